@@ -414,8 +414,7 @@ def _plain_act_grad(s):
     gu = gu.float() if s["saved_sf"] is None else _values(gu, s["saved_sf"][rows])
     g, u = gu.chunk(2, 1)
     gh = s["grad"][rows].float()
-    e = torch.exp(-g)
-    sig = 1.0 / (1.0 + e)
+    sig = 1.0 / (1.0 + torch.exp(-g))
     silu = g * sig
     whole = silu * u
     wgh = gh
@@ -423,7 +422,7 @@ def _plain_act_grad(s):
         w = s["weights"][rows][:, None]
         s["grad_weights"][rows] = (gh * whole).sum(1)
         whole, wgh = whole * w, gh * w
-    slope = sig * (1.0 + g * (e * sig))
+    slope = sig * (1.0 + g * (1.0 - sig))
     s["grad_gate_up"][rows] = torch.cat((wgh * u * slope, wgh * silu), 1).bfloat16()
     if s["h"] is not None:
         s["h"][rows] = whole.bfloat16()

@@ -318,7 +318,8 @@ def _pack(e):
 def _fp8(v, kind):
     """E4M3 codes of fp32 rows in blocks of 128 channels, and the blocks' scales."""
     b = v.reshape(v.shape[0], -1, 128)
-    s = b.abs().amax(2).clamp_min(1e-12) / E4M3_MAX
+    s = b.abs().amax(2).clamp_min(1e-12)
+    s = s / torch.full_like(s, E4M3_MAX)      # by a number, torch multiplies with its reciprocal
     if kind == "ue8m0":
         bits = s.view(torch.int32)
         e = (bits >> 23) + ((bits & 0x7FFFFF) != 0).int()

@@ -1,7 +1,8 @@
-"""MI355X (gfx950) MoE routing layout, dispatch copy and combine.
+"""MI355X (gfx950) MoE routing layout, dispatch copy and combine, and the
+operators of the expert layer around them (norm, 4-bit products, activation).
 
-A thin ctypes binding of the C ABI declared in ``include/ep.h`` and built into
-``libep.so`` next to this file (``python -m combine_ep_layout_08_amd.build``).
+A thin ctypes binding of the C ABI declared in ``include/ep.h`` and
+``include/ep_layer.h`` and built into ``libep.so`` next to this file (``python -m combine_ep_layout_08_amd.build``).
 Every step of the computation runs in the library's HIP kernels; this module
 only marshals arguments.  PyTorch supplies device memory and the current
 stream.  There is no fallback: without the built library, every entry point
@@ -30,6 +31,10 @@ __all__ = [
     "ep_dispatch_rank", "ep_dispatch_rank_quant", "ep_combine_rank", "ep_tma_aligned_rows",
     "ep_sf_packs",
     "ep_quantize_fp8", "ep_dispatch_quant", "EP_SF_F32", "EP_SF_UE8M0", "quantize_fp8",
+    "EP_W4_INT4", "EP_W4_MXFP4", "W4Weights", "ep_add_rmsnorm", "ep_add_rmsnorm_backward",
+    "ep_add_rmsnorm_backward_workspace", "ep_w4_code_bytes", "ep_w4_scale_bytes", "ep_w4_pack",
+    "ep_expert_w4", "ep_swiglu", "ep_swiglu_backward", "add_rmsnorm", "bind_add_rmsnorm",
+    "add_rmsnorm_backward", "pack_w4",
 ]
 
 LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(
@@ -41,6 +46,7 @@ LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(
 EP_BF16, EP_FP8_E4M3, EP_F32, EP_I32, EP_I64 = range(5)
 EP_DISPATCH_ZERO_PADDING, EP_DISPATCH_STREAMING = 1, 2
 EP_SF_F32, EP_SF_UE8M0 = 0, 1
+EP_W4_INT4, EP_W4_MXFP4 = 0, 1
 _SF_FORMATS = {"f32": EP_SF_F32, "ue8m0": EP_SF_UE8M0}
 EP_ERRBIT_CAPACITY = 1
 EP_ERRBIT_INVALID_ID = 2
@@ -114,6 +120,21 @@ _SIGNATURES = {
     "ep_time_next_call": (ctypes.c_int, [_P, _P]),
     "ep_combine_backward": (ctypes.c_int, [_HP, _P, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "ep_dispatch_backward": (ctypes.c_int, [_HP, _P, _I32, _P, _P, _P, _P]),
+    # ep_layer.h
+    "ep_add_rmsnorm": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, ctypes.c_float, _I32, _I32, _P, _P,
+                                      ctypes.c_int, _P, _P, _I64, _I64, _P, _P]),
+    "ep_add_rmsnorm_backward_workspace": (ctypes.c_size_t, [_I32, _I32]),
+    "ep_add_rmsnorm_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, _P, _I32, _I32, _P,
+                                               _P, _P, ctypes.c_size_t, _P]),
+    "ep_w4_code_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
+    "ep_w4_scale_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, ctypes.c_int, _I32]),
+    "ep_w4_pack": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, ctypes.c_int, _I32, _P, _P, _P]),
+    "ep_expert_w4": (ctypes.c_int, [_HP, _P, ctypes.c_int, _I32, _I32, _P, ctypes.c_int, _I64,
+                                    _I64, _P, _P, ctypes.c_int, _I32, _I32, _P, _P]),
+    "ep_swiglu": (ctypes.c_int, [_HP, _P, _I32, _P, ctypes.c_int, _P, ctypes.c_int, _P, _I64, _I64,
+                                 _P, ctypes.c_int, _P, _I64, _I64, _P]),
+    "ep_swiglu_backward": (ctypes.c_int, [_HP, _P, _I32, _P, _P, ctypes.c_int, ctypes.c_int, _P,
+                                          _I64, _I64, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -250,6 +271,63 @@ def ep_dispatch_backward(h: ep_handle, grad_out_x_ptr, hidden, grad_out_w_ptr, g
                          grad_w_ptr, stream) -> int:
     return lib().ep_dispatch_backward(ctypes.byref(h), grad_out_x_ptr, hidden, grad_out_w_ptr,
                                       grad_x_ptr, grad_w_ptr, stream)
+
+
+def ep_add_rmsnorm(x_ptr, residual_ptr, weight_ptr, weight_dtype, eps, num_tokens, hidden,
+                   out_z_ptr, out_y_ptr, fmt, out_q_ptr, out_sf_ptr, out_ts, out_hs, out_rstd_ptr,
+                   stream) -> int:
+    return lib().ep_add_rmsnorm(x_ptr, residual_ptr, weight_ptr, weight_dtype, eps, num_tokens,
+                                hidden, out_z_ptr, out_y_ptr, fmt, out_q_ptr, out_sf_ptr, out_ts,
+                                out_hs, out_rstd_ptr, stream)
+
+
+def ep_add_rmsnorm_backward_workspace(num_tokens: int, hidden: int) -> int:
+    return int(lib().ep_add_rmsnorm_backward_workspace(num_tokens, hidden))
+
+
+def ep_add_rmsnorm_backward(grad_y_ptr, z_ptr, weight_ptr, weight_dtype, rstd_ptr, grad_z_ptr,
+                            num_tokens, hidden, grad_x_ptr, grad_weight_ptr, workspace_ptr,
+                            ws_bytes, stream) -> int:
+    return lib().ep_add_rmsnorm_backward(grad_y_ptr, z_ptr, weight_ptr, weight_dtype, rstd_ptr,
+                                         grad_z_ptr, num_tokens, hidden, grad_x_ptr,
+                                         grad_weight_ptr, workspace_ptr, ws_bytes, stream)
+
+
+def ep_w4_code_bytes(num_experts: int, n: int, k: int) -> int:
+    return int(lib().ep_w4_code_bytes(num_experts, n, k))
+
+
+def ep_w4_scale_bytes(num_experts: int, n: int, k: int, fmt: int, group: int) -> int:
+    return int(lib().ep_w4_scale_bytes(num_experts, n, k, fmt, group))
+
+
+def ep_w4_pack(codes_ptr, scales_ptr, num_experts, n, k, fmt, group, out_codes_ptr,
+               out_scales_ptr, stream) -> int:
+    return lib().ep_w4_pack(codes_ptr, scales_ptr, num_experts, n, k, fmt, group, out_codes_ptr,
+                            out_scales_ptr, stream)
+
+
+def ep_expert_w4(h: ep_handle, x_ptr, x_dtype, token_rows, k, sf_ptr, sf_fmt, sf_ts, sf_hs,
+                 codes_ptr, scales_ptr, fmt, group, n, out_ptr, stream) -> int:
+    return lib().ep_expert_w4(ctypes.byref(h), x_ptr, x_dtype, token_rows, k, sf_ptr, sf_fmt,
+                              sf_ts, sf_hs, codes_ptr, scales_ptr, fmt, group, n, out_ptr, stream)
+
+
+def ep_swiglu(h: ep_handle, gate_up_ptr, inter, row_weights_ptr, h_dtype, out_h_ptr, fmt,
+              out_sf_ptr, out_ts, out_hs, saved_ptr, saved_fmt, saved_sf_ptr, saved_ts, saved_hs,
+              stream) -> int:
+    return lib().ep_swiglu(ctypes.byref(h), gate_up_ptr, inter, row_weights_ptr, h_dtype,
+                           out_h_ptr, fmt, out_sf_ptr, out_ts, out_hs, saved_ptr, saved_fmt,
+                           saved_sf_ptr, saved_ts, saved_hs, stream)
+
+
+def ep_swiglu_backward(h: ep_handle, grad_h_ptr, inter, row_weights_ptr, saved_ptr, saved_dtype,
+                       saved_fmt, saved_sf_ptr, saved_ts, saved_hs, grad_gate_up_ptr,
+                       grad_row_weights_ptr, out_h_ptr, stream) -> int:
+    return lib().ep_swiglu_backward(ctypes.byref(h), grad_h_ptr, inter, row_weights_ptr,
+                                    saved_ptr, saved_dtype, saved_fmt, saved_sf_ptr, saved_ts,
+                                    saved_hs, grad_gate_up_ptr, grad_row_weights_ptr, out_h_ptr,
+                                    stream)
 
 
 def ep_status_str(status: int) -> str:
@@ -403,6 +481,180 @@ def quantize_fp8(x: torch.Tensor, scale_format="f32", out_q=None, out_sf=None,
     _check(ep_quantize_fp8(_ptr(x), T, H, fmt, _ptr(out_q), _ptr(out_sf), ts, hs, _stream()),
            "ep_quantize_fp8")
     return out_q, out_sf
+
+
+_CODE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _here(*tensors):
+    """The calls enqueue on the current device's stream: every tensor must live there."""
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            _need(t.device.index == torch.cuda.current_device(),
+                  "tensors must be on the current device")
+
+
+def _rows_of(t, name, rows, cols, dtype):
+    """``t`` must be a contiguous device tensor [rows, cols]."""
+    _dev(t, name)
+    _need(t.dtype == dtype and tuple(t.shape) == (rows, cols),
+          f"{name} must be {dtype} [{rows}, {cols}]")
+
+
+def _norm_weight(weight, hidden) -> int:
+    _dev(weight, "weight")
+    _need(weight.dtype in (torch.bfloat16, torch.float32) and tuple(weight.shape) == (hidden,),
+          "weight must be bf16 or fp32 [H]")
+    return EP_BF16 if weight.dtype == torch.bfloat16 else EP_F32
+
+
+def _add_rmsnorm_call(x, weight, residual, eps, out_z, out_y, want_y, scale_format, out_q, out_sf,
+                      col_major_sf, want_rstd, out_rstd):
+    _dev(x, "x")
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2, "x must be bf16 [T, H]")
+    T, H = x.shape
+    wdt = _norm_weight(weight, H)
+    if residual is not None:
+        _rows_of(residual, "residual", T, H, torch.bfloat16)
+        if out_z is None:
+            out_z = torch.empty_like(x)
+    if out_z is not None:
+        _rows_of(out_z, "out_z", T, H, torch.bfloat16)
+    if want_y and out_y is None:
+        out_y = torch.empty_like(x)
+    if out_y is not None:
+        _rows_of(out_y, "out_y", T, H, torch.bfloat16)
+    fmt, ts, hs = EP_SF_F32, 0, 0
+    if scale_format is not None:
+        fmt = _sf_format(scale_format)
+        packs = ep_sf_packs(H, fmt)
+        _need(packs > 0, "hidden must be a positive multiple of 128")
+        if out_q is None:
+            out_q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+        _dev(out_q, "out_q")
+        _need(out_q.dtype in _CODE_DTYPES and tuple(out_q.shape) == (T, H),
+              "out_q must be FP8 codes [T, H]")
+        out_sf = _quant_sf_out(out_sf, T, packs, fmt, col_major_sf, x.device)
+        ts, hs = out_sf.stride()
+    else:
+        _need(out_q is None and out_sf is None, "FP8 rows need a scale_format")
+    if want_rstd and out_rstd is None:
+        out_rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    if out_rstd is not None:
+        _dev(out_rstd, "out_rstd")
+        _need(out_rstd.dtype == torch.float32 and tuple(out_rstd.shape) == (T,),
+              "out_rstd must be fp32 [T]")
+    _here(x, weight, residual, out_z, out_y, out_q, out_sf, out_rstd)
+    args = (_ptr(x), _ptr(residual), _ptr(weight), wdt, eps, T, H, _ptr(out_z), _ptr(out_y), fmt,
+            _ptr(out_q), _ptr(out_sf), ts, hs, _ptr(out_rstd))
+    return (lib().ep_add_rmsnorm, args, (out_y, out_z, out_q, out_sf, out_rstd),
+            (x, weight, residual))
+
+
+def add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out_z=None, out_y=None, want_y: bool = True,
+                scale_format=None, out_q=None, out_sf=None, col_major_sf: bool = False,
+                want_rstd: bool = False, out_rstd=None):
+    """z = x + residual (bf16 [T, H]), its root-mean-square norm times ``weight``
+    (bf16 or fp32 [H]).  Returns (y, z, codes, scales, rstd): y bf16 unless
+    ``want_y`` is false; z None without a residual (it is x then) unless
+    ``out_z`` is given; E4M3 codes and scales of the fp32 y with ``scale_format``
+    'f32' or 'ue8m0' (as quantize_fp8 makes them); rstd fp32 [T] for the backward
+    pass with ``want_rstd``."""
+    fn, args, result, _ = _add_rmsnorm_call(x, weight, residual, eps, out_z, out_y, want_y,
+                                            scale_format, out_q, out_sf, col_major_sf, want_rstd,
+                                            out_rstd)
+    _check(fn(*args, _stream()), "ep_add_rmsnorm")
+    return result
+
+
+def bind_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor,
+                     residual: Optional[torch.Tensor] = None, eps: float = 1e-6, out_z=None,
+                     out_y=None, want_y: bool = True, scale_format=None, out_q=None, out_sf=None,
+                     col_major_sf: bool = False, want_rstd: bool = False,
+                     out_rstd=None) -> "BoundCall":
+    """``add_rmsnorm`` bound to these tensors (see BoundCall)."""
+    fn, args, result, keep = _add_rmsnorm_call(x, weight, residual, eps, out_z, out_y, want_y,
+                                               scale_format, out_q, out_sf, col_major_sf,
+                                               want_rstd, out_rstd)
+    return BoundCall(fn, args, "ep_add_rmsnorm", result, keep)
+
+
+def add_rmsnorm_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Tensor,
+                         rstd: torch.Tensor, grad_residual: Optional[torch.Tensor] = None,
+                         want_grad_x: bool = True, want_grad_weight: bool = True, grad_x=None,
+                         grad_weight=None, workspace=None):
+    """Gradients of ``add_rmsnorm`` from its z and rstd.  ``grad_residual`` is the
+    gradient that reaches z along the residual.  Returns (grad_x bf16 [T, H], of
+    x and of the residual alike, or None, grad_weight fp32 [H] or None)."""
+    _dev(z, "z")
+    _need(z.dtype == torch.bfloat16 and z.dim() == 2, "z must be bf16 [T, H]")
+    T, H = z.shape
+    _rows_of(grad_y, "grad_y", T, H, torch.bfloat16)
+    wdt = _norm_weight(weight, H)
+    _dev(rstd, "rstd")
+    _need(rstd.dtype == torch.float32 and tuple(rstd.shape) == (T,), "rstd must be fp32 [T]")
+    if grad_residual is not None:
+        _rows_of(grad_residual, "grad_residual", T, H, torch.bfloat16)
+    if want_grad_x and grad_x is None:
+        grad_x = torch.empty_like(z)
+    if grad_x is not None:
+        _rows_of(grad_x, "grad_x", T, H, torch.bfloat16)
+    if want_grad_weight and grad_weight is None:
+        grad_weight = torch.empty(H, dtype=torch.float32, device=z.device)
+    nbytes = 0
+    if grad_weight is not None:
+        _dev(grad_weight, "grad_weight")
+        _need(grad_weight.dtype == torch.float32 and tuple(grad_weight.shape) == (H,),
+              "grad_weight must be fp32 [H]")
+        if workspace is None:
+            workspace = torch.empty(max(ep_add_rmsnorm_backward_workspace(T, H), 16),
+                                    dtype=torch.uint8, device=z.device)
+        _dev(workspace, "workspace")
+        nbytes = workspace.numel() * workspace.element_size()
+    _here(grad_y, z, weight, rstd, grad_residual, grad_x, grad_weight, workspace)
+    _check(ep_add_rmsnorm_backward(_ptr(grad_y), _ptr(z), _ptr(weight), wdt, _ptr(rstd),
+                                   _ptr(grad_residual), T, H, _ptr(grad_x), _ptr(grad_weight),
+                                   _ptr(workspace), nbytes, _stream()), "ep_add_rmsnorm_backward")
+    return grad_x, grad_weight
+
+
+class W4Weights:
+    """The experts' 4-bit weights in the layout of ep_expert_w4 (``pack_w4``)."""
+    __slots__ = ("codes", "scales", "num_experts", "n", "k", "format", "group")
+
+    def __init__(self, codes, scales, num_experts, n, k, fmt, group):
+        self.codes, self.scales = codes, scales
+        self.num_experts, self.n, self.k, self.format, self.group = num_experts, n, k, fmt, group
+
+
+def pack_w4(codes: torch.Tensor, scales: torch.Tensor) -> W4Weights:
+    """Lay 4-bit weights out for ``Handle.expert_w4``, once.  codes: uint8
+    [E, n, k/2], channel 2j in the low half of byte j.  scales [E, n, k/group]:
+    bf16 for codes that stand for code - 8 (group 32, 64 or 128), or uint8 /
+    float8_e8m0fnu exponents for E2M1 codes (group 32)."""
+    _dev(codes, "codes")
+    _dev(scales, "scales")
+    _need(codes.dtype == torch.uint8 and codes.dim() == 3, "codes must be uint8 [E, n, k/2]")
+    E, n, k = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    _need(scales.dim() == 3 and tuple(scales.shape[:2]) == (E, n) and scales.shape[2] > 0 and
+          k % scales.shape[2] == 0, "scales must be [E, n, k/group]")
+    group = k // scales.shape[2]
+    if scales.dtype == torch.bfloat16:
+        fmt = EP_W4_INT4
+    else:
+        _need(scales.dtype in (torch.uint8, torch.float8_e8m0fnu),
+              "scales must be bf16 (int4) or uint8 exponents (mxfp4)")
+        fmt = EP_W4_MXFP4
+    nc, ns = ep_w4_code_bytes(E, n, k), ep_w4_scale_bytes(E, n, k, fmt, group)
+    _need(nc > 0 and ns > 0, "4-bit weights: n % 8 == 0, k % 128 == 0, k <= 32768, E <= 1024, "
+          "group 32, 64 or 128 with bf16 scales and 32 with exponents")
+    out_codes = torch.empty(nc, dtype=torch.uint8, device=codes.device)
+    out_scales = torch.empty(ns, dtype=torch.uint8, device=codes.device)
+    _here(codes, scales)
+    _check(ep_w4_pack(_ptr(codes), _ptr(scales), E, n, k, fmt, group, _ptr(out_codes),
+                      _ptr(out_scales), _stream()), "ep_w4_pack")
+    return W4Weights(out_codes, out_scales, E, n, k, fmt, group)
 
 
 class Handle:
@@ -900,3 +1152,179 @@ class Handle:
         _check(ep_combine_rank(self.h, _ptr(x), H, _ptr(bias_0), _ptr(bias_1), _ptr(out),
                                _stream()), "ep_combine_rank")
         return out
+
+    # ------------------------------------------------------------ expert layer
+
+    def expert_w4(self, x: torch.Tensor, weights: W4Weights, sf: Optional[torch.Tensor] = None,
+                  token_rows: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Every expert's rows times its 4-bit weights: bf16 [capacity, n].  x: bf16
+        rows or FP8 codes with scales ``sf``, as dispatch writes them
+        ([capacity, k]), or with ``token_rows`` the tokens' own rows ([T, k]), which
+        needs no dispatch.  Rows without a slot are left as they were."""
+        fn, args, out, _ = self._expert_w4_call(x, weights, sf, token_rows, out)
+        _check(fn(*args, _stream()), "ep_expert_w4")
+        return out
+
+    def bind_expert_w4(self, x: torch.Tensor, weights: W4Weights,
+                       sf: Optional[torch.Tensor] = None, token_rows: bool = False,
+                       out: Optional[torch.Tensor] = None) -> BoundCall:
+        """``expert_w4`` bound to these tensors (see BoundCall)."""
+        fn, args, out, keep = self._expert_w4_call(x, weights, sf, token_rows, out)
+        return BoundCall(fn, args, "ep_expert_w4", out, keep, self.h)
+
+    def _expert_w4_call(self, x, weights, sf, token_rows, out):
+        rows = self.h.num_tokens if token_rows else self.capacity
+        _need(weights.num_experts == self.h.num_experts, "weights of another number of experts")
+        _dev(x, "x")
+        _need(x.dim() == 2 and tuple(x.shape) == (rows, weights.k),
+              f"x must be [{rows}, {weights.k}]")
+        fp8 = x.dtype in _CODE_DTYPES
+        _need(fp8 or x.dtype == torch.bfloat16, "x must be bf16 or FP8 e4m3")
+        fmt, ts, hs = EP_SF_F32, 0, 0
+        if fp8:
+            fmt, ts, hs = self._sf_in(sf, "sf", rows, weights.k)
+        else:
+            _need(sf is None, "scale factors are for FP8 only")
+        if out is None:
+            out = torch.empty((self.capacity, weights.n), dtype=torch.bfloat16, device=x.device)
+        _rows_of(out, "out", self.capacity, weights.n, torch.bfloat16)
+        _here(x, sf, out, weights.codes, self.workspace)
+        args = (ctypes.byref(self.h), _ptr(x), EP_FP8_E4M3 if fp8 else EP_BF16,
+                1 if token_rows else 0, weights.k, _ptr(sf), fmt, ts, hs, _ptr(weights.codes),
+                _ptr(weights.scales), weights.format, weights.group, weights.n, _ptr(out))
+        return lib().ep_expert_w4, args, out, (x, weights, sf)
+
+    @staticmethod
+    def _sf_in(sf, name, rows, cols):
+        """Format and strides of FP8 rows' scales: fp32 [rows, cols/128] or int32
+        packs of UE8M0 exponents."""
+        _need(sf is not None, "FP8 rows need scale factors")
+        _dev_strided(sf, name)
+        _need(sf.dtype in _SF_DTYPES, f"{name} must be fp32 scales or int32 packs")
+        fmt = EP_SF_F32 if sf.dtype == torch.float32 else EP_SF_UE8M0
+        packs = ep_sf_packs(cols, fmt)
+        _need(packs > 0 and tuple(sf.shape) == (rows, packs),
+              f"{name} must be [{rows}, {packs}] for FP8 rows of {cols} channels")
+        return (fmt, *sf.stride())
+
+    def _row_weights(self, row_weights):
+        if row_weights is not None:
+            _dev(row_weights, "row_weights")
+            _need(row_weights.dtype == torch.float32 and row_weights.numel() == self.capacity,
+                  "row_weights must be fp32 [capacity]")
+
+    def swiglu(self, gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = None,
+               scale_format=None, out=None, out_sf=None, checkpoint=None, saved=None,
+               saved_sf=None, col_major_sf: bool = False):
+        """silu(gate) * up (* row_weights) of the expert rows gate_up bf16
+        [capacity, 2 inter], gate first.  Returns (h, scales, saved, saved_scales): h
+        bf16 [capacity, inter], or E4M3 codes with ``scale_format`` 'f32' or 'ue8m0';
+        with ``checkpoint`` 'f32' or 'ue8m0', saved holds gate_up in E4M3 for
+        ``swiglu_backward``.  Rows without a slot are left as they were."""
+        fn, args, result, _ = self._swiglu_call(gate_up, row_weights, scale_format, out, out_sf,
+                                                checkpoint, saved, saved_sf, col_major_sf)
+        _check(fn(*args, _stream()), "ep_swiglu")
+        return result
+
+    def bind_swiglu(self, gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = None,
+                    scale_format=None, out=None, out_sf=None, checkpoint=None, saved=None,
+                    saved_sf=None, col_major_sf: bool = False) -> BoundCall:
+        """``swiglu`` bound to these tensors (see BoundCall)."""
+        fn, args, result, keep = self._swiglu_call(gate_up, row_weights, scale_format, out,
+                                                   out_sf, checkpoint, saved, saved_sf,
+                                                   col_major_sf)
+        return BoundCall(fn, args, "ep_swiglu", result, keep, self.h)
+
+    def _swiglu_call(self, gate_up, row_weights, scale_format, out, out_sf, checkpoint, saved,
+                     saved_sf, col_major_sf):
+        cap, dev = self.capacity, gate_up.device
+        _dev(gate_up, "gate_up")
+        _need(gate_up.dtype == torch.bfloat16 and gate_up.dim() == 2 and
+              gate_up.shape[0] == cap and gate_up.shape[1] % 2 == 0,
+              "gate_up must be bf16 [capacity, 2 inter]")
+        inter = gate_up.shape[1] // 2
+        self._row_weights(row_weights)
+        fmt, ts, hs = EP_SF_F32, 0, 0
+        if scale_format is None:
+            _need(out_sf is None, "FP8 rows need a scale_format")
+            if out is None:
+                out = torch.empty((cap, inter), dtype=torch.bfloat16, device=dev)
+            _rows_of(out, "out", cap, inter, torch.bfloat16)
+        else:
+            fmt = _sf_format(scale_format)
+            packs = ep_sf_packs(inter, fmt)
+            _need(packs > 0, "inter must be a positive multiple of 128")
+            if out is None:
+                out = torch.empty((cap, inter), dtype=torch.uint8, device=dev)
+            _dev(out, "out")
+            _need(out.dtype in _CODE_DTYPES and tuple(out.shape) == (cap, inter),
+                  f"out must be FP8 codes [{cap}, {inter}]")
+            out_sf = _quant_sf_out(out_sf, cap, packs, fmt, col_major_sf, dev)
+            ts, hs = out_sf.stride()
+        sfmt, sts, shs = EP_SF_F32, 0, 0
+        if checkpoint is None:
+            _need(saved is None and saved_sf is None, "saved rows need a checkpoint format")
+        else:
+            sfmt = _sf_format(checkpoint)
+            packs = ep_sf_packs(2 * inter, sfmt)
+            _need(inter % 128 == 0 and packs > 0, "inter must be a positive multiple of 128")
+            if saved is None:
+                saved = torch.empty((cap, 2 * inter), dtype=torch.uint8, device=dev)
+            _dev(saved, "saved")
+            _need(saved.dtype in _CODE_DTYPES and tuple(saved.shape) == (cap, 2 * inter),
+                  f"saved must be FP8 codes [{cap}, {2 * inter}]")
+            saved_sf = _quant_sf_out(saved_sf, cap, packs, sfmt, False, dev)
+            sts, shs = saved_sf.stride()
+        _here(gate_up, row_weights, out, out_sf, saved, saved_sf, self.workspace)
+        args = (ctypes.byref(self.h), _ptr(gate_up), inter, _ptr(row_weights),
+                EP_BF16 if scale_format is None else EP_FP8_E4M3, _ptr(out), fmt, _ptr(out_sf),
+                ts, hs, _ptr(saved), sfmt, _ptr(saved_sf), sts, shs)
+        return (lib().ep_swiglu, args, (out, out_sf, saved, saved_sf), (gate_up, row_weights))
+
+    def swiglu_backward(self, grad_h: torch.Tensor, saved: torch.Tensor,
+                        saved_sf: Optional[torch.Tensor] = None,
+                        row_weights: Optional[torch.Tensor] = None, grad_gate_up=None,
+                        grad_row_weights=None, want_grad_weights: bool = False, out=None,
+                        want_h: bool = False):
+        """Gradients of ``swiglu``.  saved: its E4M3 checkpoint with ``saved_sf``, or the
+        bf16 gate_up.  Returns (grad_gate_up bf16 [capacity, 2 inter],
+        grad_row_weights fp32 [capacity] or None, for ``dispatch_backward``, and with
+        ``want_h`` the activation made again from ``saved``, bf16 [capacity, inter],
+        or None).  Rows without a slot are left as they were."""
+        cap = self.capacity
+        _dev(grad_h, "grad_h")
+        _need(grad_h.dtype == torch.bfloat16 and grad_h.dim() == 2 and grad_h.shape[0] == cap,
+              "grad_h must be bf16 [capacity, inter]")
+        inter = grad_h.shape[1]
+        _dev(saved, "saved")
+        fp8 = saved.dtype in _CODE_DTYPES
+        _need((fp8 or saved.dtype == torch.bfloat16) and tuple(saved.shape) == (cap, 2 * inter),
+              f"saved must be bf16 or FP8 codes [{cap}, {2 * inter}]")
+        fmt, ts, hs = EP_SF_F32, 0, 0
+        if fp8:
+            _need(inter % 128 == 0, "inter must be a positive multiple of 128")
+            fmt, ts, hs = self._sf_in(saved_sf, "saved_sf", cap, 2 * inter)
+        else:
+            _need(saved_sf is None, "scale factors are for FP8 only")
+        self._row_weights(row_weights)
+        if grad_gate_up is None:
+            grad_gate_up = torch.empty((cap, 2 * inter), dtype=torch.bfloat16,
+                                       device=grad_h.device)
+        _rows_of(grad_gate_up, "grad_gate_up", cap, 2 * inter, torch.bfloat16)
+        if want_grad_weights and grad_row_weights is None:
+            grad_row_weights = torch.empty(cap, dtype=torch.float32, device=grad_h.device)
+        if grad_row_weights is not None:
+            _dev(grad_row_weights, "grad_row_weights")
+            _need(grad_row_weights.dtype == torch.float32 and grad_row_weights.numel() == cap,
+                  "grad_row_weights must be fp32 [capacity]")
+        if want_h and out is None:
+            out = torch.empty((cap, inter), dtype=torch.bfloat16, device=grad_h.device)
+        if out is not None:
+            _rows_of(out, "out", cap, inter, torch.bfloat16)
+        _here(grad_h, saved, saved_sf, row_weights, grad_gate_up, grad_row_weights, out,
+              self.workspace)
+        _check(ep_swiglu_backward(self.h, _ptr(grad_h), inter, _ptr(row_weights), _ptr(saved),
+                                  EP_FP8_E4M3 if fp8 else EP_BF16, fmt, _ptr(saved_sf), ts, hs,
+                                  _ptr(grad_gate_up), _ptr(grad_row_weights), _ptr(out),
+                                  _stream()), "ep_swiglu_backward")
+        return grad_gate_up, grad_row_weights, out

@@ -17,7 +17,7 @@ CEILINGS_LIB = os.path.join(PKG, "libep_ceilings.so")
 CEILINGS_SOURCES = ["ep_ceilings.hip"]
 
 SOURCES = ["ep_api.cpp", "ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_backward.hip",
-           "ep_rank.hip"]
+           "ep_rank.hip", "ep_layer_api.cpp", "ep_norm.hip", "ep_act.hip", "ep_w4.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

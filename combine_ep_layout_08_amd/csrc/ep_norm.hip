@@ -1,0 +1,233 @@
+// Sum with the residual, root-mean-square norm and E4M3 rows, and the norm's
+// gradient, on gfx950 (include/ep_layer.h: ep_add_rmsnorm).
+#include "ep_layer_internal.h"
+#include "ep_rows.h"
+
+namespace ep {
+namespace {
+
+constexpr int kNormBlocks = 1 << 18;     // most blocks of a launch; they walk the rows behind
+
+// Channels [8v, 8v + 8) of the norm's weight as binary32.
+__device__ inline void load_weight(const void *w, bool bf16, int v, float f[8]) {
+    if (bf16) {
+        unpack8(static_cast<const u32x4 *>(w)[v], f);
+    } else {
+        const f32x4 *p = static_cast<const f32x4 *>(w) + 2 * static_cast<int64_t>(v);
+        const f32x4 a = p[0], b = p[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- forward
+// One block a row; thread t holds the row's 16-byte vectors t, t + threads,
+// ... (VPT of them) in registers, so the row is read once.  A wave holds 512
+// consecutive channels of each pass: four scale blocks, one a row of 16 lanes,
+// and one whole UE8M0 pack.
+template <int VPT, int FMT>
+__global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
+#pragma clang fp contract(off)
+    __shared__ double sums[2][16];
+    const int V = a.hidden / 8;
+    const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 63;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.num_tokens; row += gridDim.x, turn ^= 1) {
+        const u32x4 *x = static_cast<const u32x4 *>(a.x) + row * V;
+        const u32x4 *res = a.residual ? static_cast<const u32x4 *>(a.residual) + row * V : nullptr;
+        u32x4 z[VPT];
+        float w[VPT][8];
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            z[i] = u32x4{0u, 0u, 0u, 0u};
+            if (v < V) {
+                z[i] = x[v];
+                if (res) {
+                    float f[8], g[8];
+                    unpack8(z[i], f);
+                    unpack8(res[v], g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] += g[j];
+                    z[i] = pack8(f);
+                }
+                load_weight(a.weight, a.weight_bf16, v, w[i]);
+                if (a.out_z) (static_cast<u32x4 *>(a.out_z) + row * V)[v] = z[i];
+            }
+            float f[8];
+            unpack8(z[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(f[j]),
+                                                            static_cast<double>(f[j]), sum);
+        }
+        sum = wave_sum64(sum);
+        if (lane == 0) sums[turn][tid >> 6] = sum;
+        __syncthreads();                   // the other half of sums is free until the next barrier
+        sum = 0.0;
+        for (int i = 0; i < threads / 64; ++i) sum += sums[turn][i];
+        const float rstd = static_cast<float>(
+            1.0 / __builtin_sqrt(sum / static_cast<double>(a.hidden) + static_cast<double>(a.eps)));
+        if (a.out_rstd && tid == 0) a.out_rstd[row] = rstd;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            float y[8];
+            unpack8(z[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = v < V ? (y[j] * rstd) * w[i][j] : 0.0f;
+            if (a.out_y && v < V) (static_cast<u32x4 *>(a.out_y) + row * V)[v] = pack8(y);
+            if (FMT != kSfNone) {
+                uint32_t pack;
+                const u32x2 q = e4m3_block8<FMT == kSfNone ? EP_SF_F32 : FMT>(y, &pack);
+                if (v < V) (static_cast<u32x2 *>(a.out_q) + row * V)[v] = q;
+                store_packs<FMT == kSfNone ? EP_SF_F32 : FMT>(
+                    a.sf.p, a.sf.ts, a.sf.hs, row, (v - lane) / 16, V / 16, pack, lane);
+            }
+        }
+    }
+}
+
+template <int FMT>
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
+    const int V = a.hidden / 8;
+    const int vpt = V <= 512 ? 1 : V <= 1024 ? 2 : 4;
+    const int threads = ((V + vpt - 1) / vpt + 63) / 64 * 64;
+    const dim3 grid(a.num_tokens < kNormBlocks ? a.num_tokens : kNormBlocks), block(threads);
+    if (vpt == 1) norm_kernel<1, FMT><<<grid, block, 0, stream>>>(a);
+    else if (vpt == 2) norm_kernel<2, FMT><<<grid, block, 0, stream>>>(a);
+    else norm_kernel<4, FMT><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- gradient
+// Blocks walk the rows with the grid's stride; each thread keeps the weight
+// and its sums of g * n for its channels in registers, so grad_weight costs
+// one row of binary32 a block, added up by a second kernel in block order.
+template <int VPT>
+__global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a) {
+    __shared__ float sums[2][16];
+    const int V = a.hidden / 8;
+    const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 63;
+    const float inv = 1.0f / static_cast<float>(a.hidden);
+    float w[VPT][8], gw[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * threads + tid;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[i][j] = gw[i][j] = 0.0f;
+        if (v < V) load_weight(a.weight, a.weight_bf16, v, w[i]);
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.num_tokens; row += gridDim.x, turn ^= 1) {
+        const u32x4 *zr = static_cast<const u32x4 *>(a.z) + row * V;
+        const u32x4 *gr = static_cast<const u32x4 *>(a.grad_y) + row * V;
+        const float rstd = a.rstd[row];
+        u32x4 z[VPT], g[VPT], more[VPT];
+        float c = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            z[i] = g[i] = more[i] = u32x4{0u, 0u, 0u, 0u};
+            if (v < V) {
+                z[i] = zr[v];
+                g[i] = gr[v];
+                if (a.grad_z) more[i] = (static_cast<const u32x4 *>(a.grad_z) + row * V)[v];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float zf[8], gf[8];
+            unpack8(z[i], zf);
+            unpack8(g[i], gf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float gn = gf[j] * (zf[j] * rstd);
+                gw[i][j] += gn;
+                c = __builtin_fmaf(gn, w[i][j], c);
+            }
+        }
+        if (!a.grad_x) continue;
+        c = wave_sum(c);
+        if (lane == 0) sums[turn][tid >> 6] = c;
+        __syncthreads();               // the other half of sums is free until the next barrier
+        c = 0.0f;
+        for (int i = 0; i < threads / 64; ++i) c += sums[turn][i];
+        c *= inv;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            if (v >= V) continue;
+            float zf[8], gf[8], mf[8], o[8];
+            unpack8(z[i], zf);
+            unpack8(g[i], gf);
+            unpack8(more[i], mf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = __builtin_fmaf(gf[j] * w[i][j] - (zf[j] * rstd) * c, rstd, mf[j]);
+            (static_cast<u32x4 *>(a.grad_x) + row * V)[v] = pack8(o);
+        }
+    }
+    if (!a.grad_weight) return;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * threads + tid;
+        if (v >= V) continue;
+        f32x4 *p = reinterpret_cast<f32x4 *>(a.partial +
+                                             static_cast<int64_t>(blockIdx.x) * a.hidden) + 2 * v;
+        p[0] = f32x4{gw[i][0], gw[i][1], gw[i][2], gw[i][3]};
+        p[1] = f32x4{gw[i][4], gw[i][5], gw[i][6], gw[i][7]};
+    }
+}
+
+// Sums of the blocks' rows: 16 lanes of 4 channels, 16 groups of rows a block.
+__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float *partial, int rows,
+                                                            int hidden, float *out) {
+    __shared__ f32x4 sums[16][16];
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const int c = (blockIdx.x * 16 + lane) * 4;
+    f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < hidden)
+        for (int r = group; r < rows; r += 16)
+            s += *reinterpret_cast<const f32x4 *>(partial + static_cast<int64_t>(r) * hidden + c);
+    sums[group][lane] = s;
+    __syncthreads();
+    if (group != 0 || c >= hidden) return;
+    for (int g = 1; g < 16; ++g) s += sums[g][lane];
+    *reinterpret_cast<f32x4 *>(out + c) = s;
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream) {
+    if (!a.out_q) return launch_norm<kSfNone>(a, stream);
+    return a.sf.ue8m0 ? launch_norm<EP_SF_UE8M0>(a, stream) : launch_norm<EP_SF_F32>(a, stream);
+}
+
+int norm_grad_blocks(int32_t num_tokens, int32_t hidden) {
+    (void)hidden;
+    return num_tokens < 512 ? num_tokens : 512;
+}
+
+hipError_t launch_add_rmsnorm_backward(const NormGradArgs &a, hipStream_t stream) {
+    const int V = a.hidden / 8;
+    const int blocks = norm_grad_blocks(a.num_tokens, a.hidden);
+    if (blocks > 0) {
+        const int vpt = V <= 512 ? 1 : V <= 1024 ? 2 : 4;
+        const int threads = ((V + vpt - 1) / vpt + 63) / 64 * 64;
+        if (vpt == 1) norm_grad_kernel<1><<<blocks, threads, 0, stream>>>(a);
+        else if (vpt == 2) norm_grad_kernel<2><<<blocks, threads, 0, stream>>>(a);
+        else norm_grad_kernel<4><<<blocks, threads, 0, stream>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (!a.grad_weight) return hipSuccess;
+    norm_grad_sum_kernel<<<(a.hidden + 63) / 64, 256, 0, stream>>>(a.partial, blocks, a.hidden,
+                                                                   a.grad_weight);
+    return hipGetLastError();
+}
+
+}  // namespace ep

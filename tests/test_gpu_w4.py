@@ -1,0 +1,263 @@
+"""ep_expert_w4 and ep_w4_pack against binary64, on the GPU.
+
+Tolerance: one rounding to bf16 (2^-8 of the value), and binary32 sums: a
+matrix instruction adds 32 products to its accumulator, at most 33 roundings of
+partial sums, and the steps' sums follow.  The partial sums are bounded by the
+sum of |x w|; with EP_W4_INT4 the codes enter as 128 + code and 136 is taken off,
+so there they are bounded by the sum of 136 |x scale| within the group."""
+import pytest
+import torch
+
+import combine_ep_layout_08_amd as ep
+from tests import layer_ref as ref
+from tests.gpu_util import needs_gpu, say
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+INT4, MX = ep.EP_W4_INT4, ep.EP_W4_MXFP4
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _x(rows, k, kind, gen):
+    x = torch.randn((rows, k), generator=gen, device="cuda").bfloat16()
+    if kind == "bf16":
+        return x, None, x.double()
+    if rows == 0:
+        return x.view(torch.uint8)[:, :k], None, x.double()
+    q, sf = ep.quantize_fp8(x, kind)
+    return q, sf, ref.code_values(q, sf)
+
+
+def _check(h, idx, x64, w64, scale64, out, token_rows, what):
+    """Rows of ``out`` against x64 . w64, others untouched."""
+    rows, expert, token = ref.rows_of(h, idx)
+    for e in torch.unique(expert).tolist():
+        mine = expert == e
+        src = x64[token[mine] if token_rows else rows[mine]]
+        want = src @ w64[e].t()
+        size = src.abs() @ (w64[e].abs() if scale64 is None else scale64[e] * 136.0).t()
+        tol = want.abs() * ref.BF16 + size * 66 * ref.F32 + 1e-38
+        got = out[rows[mine]]
+        ref.assert_close(got, want, tol, f"{what}, expert {e}")
+        norm = float(want.norm())
+        if norm > 0 and want.numel() > 64:
+            assert float((got.double() - want).norm()) < ref.BF16 * norm
+    assert ref.untouched(out, rows)
+
+
+def _scales64(scales, group, fmt):
+    return scales.double().abs().repeat_interleave(group, 2) if fmt == INT4 else None
+
+
+CASES = [  # T, K, E, A, k, n, format, group, x, token rows, empty
+    (1, 1, 1, 1, 128, 8, INT4, 128, "bf16", False, 0.0),
+    (1, 1, 1, 1, 128, 16, MX, 32, "bf16", True, 0.0),
+    (1, 8, 64, 1, 7168, 512, INT4, 128, "bf16", True, 0.0),
+    (1, 8, 16, 1, 2048, 264, MX, 32, "f32", False, 0.0),
+    (2, 2, 5, 1, 256, 24, INT4, 64, "bf16", False, 0.0),
+    (7, 3, 6, 8, 384, 40, INT4, 32, "bf16", True, 0.2),
+    (16, 1, 1, 1, 640, 72, INT4, 64, "f32", False, 0.0),
+    (17, 1, 1, 4, 896, 136, MX, 32, "bf16", False, 0.0),
+    (64, 4, 16, 1, 256, 512, INT4, 32, "bf16", False, 0.1),
+    (64, 4, 16, 128, 1152, 200, INT4, 128, "ue8m0", False, 0.1),
+    (33, 2, 2, 1, 512, 104, INT4, 64, "ue8m0", True, 0.1),
+    (65, 1, 1, 16, 1024, 48, MX, 32, "ue8m0", True, 0.0),
+    (100, 8, 8, 1, 768, 96, INT4, 128, "f32", False, 0.0),
+    (130, 2, 2, 1, 256, 8, MX, 32, "f32", True, 0.2),
+    (200, 4, 4, 64, 128, 24, INT4, 32, "f32", True, 0.0),
+    (128, 8, 64, 128, 2048, 1024, MX, 32, "f32", False, 0.0),
+    (96, 8, 300, 8, 256, 64, INT4, 64, "bf16", False, 0.1),
+    (3, 2, 1000, 1, 128, 16, INT4, 128, "bf16", True, 0.0),
+    (5, 2, 4, 1, 32768, 32, INT4, 128, "f32", False, 0.0),
+    (300, 1, 3, 1, 1920, 80, INT4, 64, "bf16", False, 0.0),
+]
+
+
+@pytest.mark.parametrize("T,K,E,A,k,n,fmt,group,kind,token_rows,empty", CASES)
+def test_product(T, K, E, A, k, n, fmt, group, kind, token_rows, empty):
+    say("w4", T, K, E, A, k, n, fmt, group, kind, token_rows, empty)
+    gen = _gen(T + k + n)
+    idx = ref.ids(T, K, E, gen, "cuda", empty)
+    h = ep.Handle(T, K, E, A)
+    h.layout(idx)
+    codes, scales = ref.random_w4(E, n, k, fmt, group, gen, "cuda")
+    w64 = ref.w4_values(codes, scales, group)
+    rows = T if token_rows else h.capacity
+    x, sf, x64 = _x(rows, k, kind, gen)
+    if not token_rows:                       # what no slot holds would spoil any sum
+        gap = torch.ones(rows, dtype=torch.bool, device="cuda")
+        gap[ref.rows_of(h, idx)[0]] = False
+        if kind == "bf16":
+            x[gap] = float("nan")
+        else:
+            x[gap] = 0x7F
+    packed = ep.pack_w4(codes, scales)
+    assert (packed.num_experts, packed.n, packed.k, packed.group) == (E, n, k, group)
+    out = ref.poisoned((h.capacity, n), torch.bfloat16)
+    got = h.expert_w4(x, packed, sf=sf, token_rows=token_rows, out=out)
+    assert got is out
+    _check(h, idx, x64, w64, _scales64(scales, group, fmt), out, token_rows, "product")
+    again = ref.poisoned((h.capacity, n), torch.bfloat16)
+    h.expert_w4(x, packed, sf=sf, token_rows=token_rows, out=again)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt,group", [(INT4, 32), (INT4, 64), (INT4, 128), (MX, 32)])
+def test_every_code_and_channel(fmt, group):
+    """One-hot rows read single weights back: every code value at every channel's
+    place, through every lane and record (exact: one product, a power of two)."""
+    k, n, T = 384, 40, 384
+    codes = (torch.arange(n * k, device="cuda").reshape(1, n, k) * 7 % 16).to(torch.uint8)
+    both = (codes[..., 0::2] | (codes[..., 1::2] << 4)).contiguous()
+    if fmt == INT4:
+        scales = torch.exp2((torch.arange(n * k // group, device="cuda") % 5).float()).reshape(
+            1, n, -1).bfloat16()
+    else:
+        scales = (120 + torch.arange(n * k // group, device="cuda") % 11).reshape(
+            1, n, -1).to(torch.uint8)
+    w64 = ref.w4_values(both, scales, group)
+    idx = torch.zeros((T, 1), dtype=torch.int64, device="cuda")
+    h = ep.Handle(T, 1, 1, 1)
+    h.layout(idx)
+    x = torch.eye(k, device="cuda").bfloat16()
+    y = h.expert_w4(x, ep.pack_w4(both, scales))
+    assert torch.equal(y.double(), w64[0].t().contiguous())
+
+
+def test_mxfp4_exponents():
+    """The whole range of exponents that bf16 holds, and 255, which makes NaN."""
+    k, n = 128, 256
+    codes = torch.full((1, n, k // 2), 0x22, dtype=torch.uint8, device="cuda")      # ones
+    e = torch.arange(256, device="cuda").reshape(1, n, 1).expand(1, n, 4)
+    scales = e.to(torch.uint8).contiguous()
+    h = ep.Handle(1, 1, 1, 1)
+    h.layout(torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+    x = torch.zeros((1, k), device="cuda").bfloat16()
+    x[0, 40] = 1.0
+    y = h.expert_w4(x, ep.pack_w4(codes, scales.view(torch.float8_e8m0fnu)))[0].double()
+    want = torch.exp2(torch.arange(255, device="cuda").double() - 127.0)
+    normal = torch.arange(255, device="cuda") >= 1
+    assert torch.equal(y[:255][normal], want[normal])
+    assert float(y[0]) in (0.0, 2.0 ** -127) and bool(y[255].isnan())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rows_with_infinities_and_nan(kind):
+    """A row that holds an infinity or a NaN does not reach the other rows."""
+    T, k, n = 20, 256, 32
+    gen = _gen(4)
+    codes, scales = ref.random_w4(2, n, k, INT4, 64, gen, "cuda")
+    idx = torch.zeros((T, 1), dtype=torch.int64, device="cuda")
+    h = ep.Handle(T, 1, 2, 1)
+    h.layout(idx)
+    x = torch.randn((T, k), generator=gen, device="cuda").bfloat16()
+    packed = ep.pack_w4(codes, scales)
+    q, sf = (x, None) if kind == "bf16" else ep.quantize_fp8(x, kind)
+    want = h.expert_w4(q, packed, sf=sf, token_rows=True)
+    bad = q.clone()
+    if kind == "bf16":
+        bad[3, 100] = float("inf")
+        bad[9, 7] = float("nan")
+    else:
+        bad[3, 100] = bad[9, 7] = 0x7F
+    got = h.expert_w4(bad, packed, sf=sf, token_rows=True)
+    keep = [t for t in range(T) if t not in (3, 9)]
+    assert torch.equal(got[keep], want[keep])
+    assert bool(got[3].isnan().all()) and bool(got[9].isnan().all())
+
+
+def test_same_expert_twice_in_a_token():
+    gen = _gen(5)
+    idx = torch.tensor([[1, 1, 0], [2, 1, 1]], device="cuda")
+    h = ep.Handle(2, 3, 3, 4, capacity=24)
+    h.layout(idx)
+    codes, scales = ref.random_w4(3, 48, 256, MX, 32, gen, "cuda")
+    x, sf, x64 = _x(2, 256, "bf16", gen)
+    out = ref.poisoned((24, 48), torch.bfloat16)
+    h.expert_w4(x, ep.pack_w4(codes, scales), token_rows=True, out=out)
+    _check(h, idx, x64, ref.w4_values(codes, scales, 32), None, out, True, "twice")
+
+
+@pytest.mark.parametrize("popular", [0, 3, 7])
+def test_all_rows_on_one_expert(popular):
+    """Skewed as far as it goes, the experts before and behind it empty."""
+    T, E, k, n = 150, 8, 512, 56
+    gen = _gen(6)
+    idx = torch.full((T, 1), popular, dtype=torch.int32, device="cuda")
+    h = ep.Handle(T, 1, E, 16)
+    h.layout(idx)
+    codes, scales = ref.random_w4(E, n, k, INT4, 128, gen, "cuda")
+    x, sf, x64 = _x(h.capacity, k, "f32", gen)
+    out = ref.poisoned((h.capacity, n), torch.bfloat16)
+    h.expert_w4(x, ep.pack_w4(codes, scales), sf=sf, out=out)
+    _check(h, idx, x64, ref.w4_values(codes, scales, 128), _scales64(scales, 128, INT4), out,
+           False, "one expert")
+
+
+def test_strided_scale_rows():
+    gen = _gen(7)
+    T, k, n = 30, 1152, 64
+    idx = ref.ids(T, 2, 4, gen, "cuda")
+    h = ep.Handle(T, 2, 4, 8)
+    h.layout(idx)
+    codes, scales = ref.random_w4(4, n, k, INT4, 32, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    x = torch.randn((T, k), generator=gen, device="cuda").bfloat16()
+    for kind in ("f32", "ue8m0"):
+        q, sf = ep.quantize_fp8(x, kind)
+        ex, esf, _ = h.dispatch(q, sf=sf, col_major_sf=True)
+        assert esf.stride(0) == 1
+        a = h.expert_w4(ex, packed, sf=esf)
+        b = h.expert_w4(q, packed, sf=sf, token_rows=True)
+        rows = ref.rows_of(h, idx)[0]
+        assert torch.equal(a[rows], b[rows])
+
+
+def test_void_layout_and_no_tokens_write_nothing():
+    gen = _gen(8)
+    codes, scales = ref.random_w4(8, 16, 128, MX, 32, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    h = ep.Handle(32, 4, 8, 1, capacity=64)
+    h.layout(ref.ids(32, 4, 8, gen, "cuda"))
+    out = ref.poisoned((64, 16), torch.bfloat16)
+    h.expert_w4(torch.ones((64, 128), device="cuda").bfloat16(), packed, out=out)
+    assert ref.untouched(out, [])
+    h.layout(torch.empty((0, 4), dtype=torch.int64, device="cuda"))
+    h.expert_w4(torch.ones((64, 128), device="cuda").bfloat16(), packed, out=out)
+    assert ref.untouched(out, [])
+    h.layout(torch.full((9, 4), -1, dtype=torch.int64, device="cuda"))
+    h.expert_w4(torch.ones((64, 128), device="cuda").bfloat16(), packed, out=out)
+    assert ref.untouched(out, [])
+
+
+def test_bound_call_and_graph():
+    """Bound and captured, the product follows new routing and new rows; every
+    replay is compared with the eager calls."""
+    gen = _gen(9)
+    T, K, E, k, n = 24, 4, 16, 512, 96
+    codes, scales = ref.random_w4(E, n, k, INT4, 64, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    idx = ref.ids(T, K, E, gen, "cuda")
+    x = torch.randn((T, k), generator=gen, device="cuda").bfloat16()
+    h, ref_h = ep.Handle(T, K, E, 8), ep.Handle(T, K, E, 8)
+    lay = h.bind_layout(idx)
+    lay()
+    out = torch.zeros((h.capacity, n), dtype=torch.bfloat16, device="cuda")
+    call = h.bind_expert_w4(x, packed, token_rows=True, out=out)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lay()
+        call()
+    for _ in range(3):
+        idx.copy_(ref.ids(T, K, E, gen, "cuda", 0.2))
+        x.copy_(torch.randn((T, k), generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref_h.layout(idx)
+        want = ref_h.expert_w4(x, packed, token_rows=True)
+        rows = ref.rows_of(ref_h, idx)[0]
+        assert torch.equal(out[rows], want[rows])

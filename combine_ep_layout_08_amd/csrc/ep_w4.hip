@@ -7,18 +7,25 @@
 // each, and accumulates rows 4 (l / 16) .. + 3 of output l % 16).
 //
 // Packed weights: for every expert, tile of 16 outputs and step of 128
-// channels, one record of 1 KB: lane l's 16 bytes at 16 l, dword j the eight
-// codes of output l % 16, channels 32 j + 8 (l / 16) .. + 7, which is what lane l
-// feeds to the j-th matrix instruction.  A wave reads a record in one load
-// of consecutive addresses, and a tile's records follow each other.  Codes of
-// EP_W4_INT4 are stored with channel 2i in nibble i and 2i + 1 in nibble i + 4, so
-// that one shift and one and-or make a pair of bf16: 0x4300 | code is 128 + code
-// exactly.  The 136 = 128 + 8 is taken off again by a product of x with the
-// constant -136, which starts the same accumulator.  EP_W4_MXFP4 codes keep
-// their order and become bf16 pairs, scaled, by v_cvt_scalef32_pk_bf16_fp4
-// (exact: E2M1 times a power of two).
-// Scales: [expert][tile][step][output][128 / group], so a lane's scales of a step
-// are consecutive.
+// channels, one record of 1 KB: lane l's 16 bytes at 16 l, dword j eight codes of
+// output l % 16.  A wave reads a record in one load of consecutive addresses, and a
+// tile's records follow each other, so a wave reads one stream (read this way
+// 1 GB came in at 7.0 TB/s on MI355X; rows of codes as they are in a model's
+// file, 16 rows by 128 bytes a wave, at 5.6 to 6.3).
+//   EP_W4_INT4: dword j holds channels 32 j + 8 (l / 16) .. + 7, what lane l feeds to the
+//   j-th instruction, channel 2i in nibble i and 2i + 1 in nibble i + 4: one shift
+//   and one and-or make a pair of bf16, 0x4300 | code = 128 + code exactly.  The
+//   136 = 128 + 8 is taken off by a product of x with the constant -136, from
+//   which the accumulators of all tiles start; a group's sum is then
+//   scaled and added to the total.  28 vector instructions a record: the
+//   conversion is what bounds larger batches.
+//   EP_W4_MXFP4: lane l holds channels 32 (l / 16) .. + 31, one scale group, in order.
+//   With x in E4M3 the codes go as they are into
+//   v_mfma_scale_f32_16x16x128_f8f6f4, which applies the group's exponent (its E4M3
+//   operand has channels 64 h + 16 (l / 16) .. + 15 in half h); with x in bf16
+//   v_cvt_scalef32_pk_bf16_fp4 makes bf16 pairs, exactly.
+// Scales: [expert][tile][step], in a step [output][group] for EP_W4_INT4 and
+// [group][output] for EP_W4_MXFP4, so a lane's scales of a step are consecutive.
 #include "ep_layer_internal.h"
 #include "ep_rows.h"
 
@@ -35,16 +42,18 @@ __device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // Eight codes as 128 + code in bf16.
-__device__ inline u32x4 int4_plus128(uint32_t w) {
+// `mask` and `one28` hold 0x000F000F and 0x43004300 in registers of the two kinds that
+// one v_and_or_b32 can take (it has no room for literals).
+__device__ inline u32x4 int4_plus128(uint32_t w, uint32_t mask, uint32_t one28) {
     u32x4 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    for (int i = 0; i < 4; ++i) o[i] = ((w >> (4 * i)) & mask) | one28;
     return o;
 }
 
 // Eight E2M1 codes times 2^(e - 127) in bf16; e = 255 gives NaN.
 __device__ inline u32x4 mxfp4(uint32_t w, uint32_t e) {
-    const float s = __uint_as_float(e == 0 ? 0x00400000u : e << 23);
+    const float s = __uint_as_float(e << 23);      // only the exponent counts: 0 is 2^-127
     u32x4 o;
     o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
     o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
@@ -64,6 +73,13 @@ __device__ inline u32x4 e4m3_bf16(u32x2 w) {
 }
 
 // ---------------------------------------------------------------- layout
+// First of the eight channels that dword j of a lane's codes holds within a
+// step: the scale groups of EP_W4_INT4 lie across a matrix instruction's lanes, the
+// ones of EP_W4_MXFP4 within a lane.
+__device__ inline int first_channel(bool int4, int j, int q) {
+    return int4 ? 32 * j + 8 * q : 32 * q + 8 * j;
+}
+
 // One thread a dword of the packed codes.
 __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *codes, int64_t experts,
                                                          int n, int k, bool int4, uint32_t *out) {
@@ -74,9 +90,8 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *codes, i
         const int j = static_cast<int>(i & 3), lane = static_cast<int>(i >> 2) & 63;
         const int64_t record = i >> 8;
         const int64_t e = record / (static_cast<int64_t>(tiles) * steps);
-        const int tile = static_cast<int>(record / steps % tiles);
-        const int row = tile * 16 + (lane & 15);
-        const int ch = static_cast<int>(record % steps) * 128 + 32 * j + 8 * (lane >> 4);
+        const int row = static_cast<int>(record / steps % tiles) * 16 + (lane & 15);
+        const int ch = static_cast<int>(record % steps) * 128 + first_channel(int4, j, lane >> 4);
         uint32_t w = int4 ? 0x88888888u : 0u;                  // zeros
         if (row < n)
             w = *reinterpret_cast<const uint32_t *>(codes + (e * n + row) * (k / 2) + ch / 2);
@@ -91,7 +106,8 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *codes, i
     }
 }
 
-// One thread a scale; U: its bytes.
+// One thread a scale; U: its bytes.  A record's scales are [output][group] for
+// EP_W4_INT4 and [group][output], lane by lane, for EP_W4_MXFP4.
 template <typename U>
 __global__ __launch_bounds__(256) void pack_scales_kernel(const U *scales, int64_t experts, int n,
                                                           int groups, int per_step, U *out) {
@@ -99,126 +115,422 @@ __global__ __launch_bounds__(256) void pack_scales_kernel(const U *scales, int64
     const int64_t total = experts * tiles * 16 * groups;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += stride) {
-        const int g = static_cast<int>(i % per_step);
-        const int64_t at = i / per_step;
-        const int64_t record = at >> 4;
+        const int at = static_cast<int>(i % (16 * per_step));
+        const int64_t record = i / (16 * per_step);
         const int64_t e = record / (static_cast<int64_t>(tiles) * steps);
-        const int row = static_cast<int>(record / steps % tiles) * 16 + static_cast<int>(at & 15);
-        const int group = static_cast<int>(record % steps) * per_step + g;
+        const bool int4 = sizeof(U) == 2;
+        const int row = static_cast<int>(record / steps % tiles) * 16 +
+                        (int4 ? at / per_step : at & 15);
+        const int group = static_cast<int>(record % steps) * per_step +
+                          (int4 ? at % per_step : at >> 4);
         out[i] = row < n ? scales[(e * n + row) * groups + group] : U(0);
     }
 }
 
 // ---------------------------------------------------------------- product
-// The expert with the a-th smallest index among those that have rows (-1 if
-// fewer have), its first row and its rows' count.  Every lane calls this.
-__device__ inline int active_expert(const int32_t *counts, const int32_t *psum, int experts, int a,
-                                    int lane, int *start, int *rows) {
+// Every expert's rows are taken in passes of `per` rows.  Pass number `pass` of all of
+// them, experts in order: its expert (-1 behind the last pass), and where its rows
+// lie.  Every lane of the wave calls this.
+struct Pass {
+    int expert, start, rows;
+};
+
+__device__ inline Pass find_pass(const int32_t *counts, const int32_t *psum, int experts, int pass,
+                                 int per, int lane) {
     for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
         const int32_t c = e < experts ? counts[e] : 0;
         const int32_t p = e < experts ? psum[e] : 0;
-        uint64_t some = __ballot(c > 0);
-        const int n = __popcll(some);
-        if (a >= n) {
-            a -= n;
+        int upto = (c + per - 1) / per;              // passes up to and with this expert
+        const uint64_t some = __ballot(upto > 0);
+        if (__ballot(upto > 1) == 0) {
+            upto = __popcll(some & ((uint64_t(2) << lane) - 1));
+        } else {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int below = __shfl_up(upto, d);
+                if (lane >= d) upto += below;
+            }
+        }
+        const int all = __builtin_amdgcn_readlane(upto, 63);
+        if (pass >= all) {
+            pass -= all;
             continue;
         }
-        for (; a > 0; --a) some &= some - 1;
-        const int l = __ffsll(static_cast<unsigned long long>(some)) - 1;
-        *start = __builtin_amdgcn_readlane(p, l);
-        *rows = __builtin_amdgcn_readlane(c, l);
-        return e0 + l;
+        // the first lane whose sum is past the number
+        const int l = __builtin_amdgcn_readfirstlane(
+            __ffsll(static_cast<unsigned long long>(__ballot(upto > pass))) - 1);
+        const int rows = __builtin_amdgcn_readlane(c, l);
+        const int before = __builtin_amdgcn_readlane(upto, l) - (rows + per - 1) / per;
+        const int first = (pass - before) * per;
+        return {e0 + l, __builtin_amdgcn_readlane(p, l) + first,
+                rows - first < per ? rows - first : per};
     }
-    return -1;
+    return {-1, 0, 0};
 }
 
 constexpr int kW4Threads = 256;
+constexpr int kW4Waves = kW4Threads / 64;
 
-// One wave for a tile of 16 outputs of one expert, 16 rows at a time.
-template <int FMT, int GROUP, bool FP8>
-__global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args a) {
+// A barrier that orders LDS alone: loads of weights stay in flight across it.
+__device__ inline void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// 16 outputs x 16 rows x 128 channels of E2M1 weights, scaled by 2^(scale - 127) in
+// each lane's 32 channels, and E4M3 codes of x.
+__device__ inline f32x4 mfma_mx(u32x4 w, uint32_t scale, u32x4 x0, u32x4 x1, f32x4 c) {
+    const i32x8 a = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+    const i32x8 b = {(int)x0.x, (int)x0.y, (int)x0.z, (int)x0.w,
+                     (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, scale, 0, 127);
+}
+
+// What a wave has read of its weights for one step: NT records and their scales.
+template <int FMT, int GROUP, int NT>
+struct Records {
+    static constexpr int kScaleWords = FMT == EP_W4_MXFP4 ? 1 : 256 / GROUP;
+    u32x4 w[NT];
+    uint32_t sw[NT][kScaleWords];
+};
+
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+// A view of `bytes` bytes; loads behind them give 0.
+__device__ inline Buffer bounded(const char *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, bytes, 0x00020000);
+}
+
+constexpr int kStream = 2;                       // non-temporal
+constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
+
+// One block for one pass (MT tiles of 16 rows of one expert) and NW groups of NT
+// tiles of 16 outputs: a group is one wave's, or KS waves take every KS-th step
+// each and add up through LDS.  The weights are operand A and x operand B, so a
+// lane holds outputs 4 (l / 16) .. + 3 of row l % 16: one scale of x a lane, the weights'
+// scales of its four outputs consecutive, and 8-byte stores.
+//   x is brought by the block's waves together and handed over through LDS, in
+//   the lanes' order (16 bytes a lane, no bank conflicts): loads of 16 rows by 64
+//   bytes keep the address units busy for about 35 cycles each, as long as 400
+//   bytes of weights take at the HBM's rate, and with every wave loading its own x a batch of
+//   16 rows an expert took 290 us instead of 165 (64 experts, 4096 x 7168, MXFP4).
+//   The weights of the next D - 1 rounds stay in flight across the rounds'
+//   barriers, which order LDS only.
+template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
+__global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int passes) {
+    typedef Records<FMT, GROUP, NT> R;
+    constexpr bool MX = FMT == EP_W4_MXFP4;
+    constexpr bool DIRECT = MX && FP8;           // codes go to the matrix instruction as they are
+    constexpr int NW = kW4Waves / KS;
+    constexpr int P = MX ? 1 : 128 / GROUP;      // groups of a step that are scaled afterwards
+    constexpr int U = DIRECT ? 2 : 4;            // 16-byte units of x a lane, row and step
+    constexpr int F = MT * U;                    // units of x a lane and round
+    constexpr int PER = F > NW ? F / NW : 1;     // of them a wave brings
+    constexpr int SPER = MT > NW ? MT / NW : 1;  // tiles' scales of x it brings
+    constexpr int kXUnits = D * KS * F * 64;
+    constexpr int kSumUnits = KS == 1 ? 0 : kW4Waves * NT * MT * 64;
+    __shared__ u32x4 lds[kXUnits > kSumUnits ? kXUnits : kSumUnits];
+    __shared__ float lds_sf[FP8 ? D * KS * MT * 16 : 1];
     const int lane = threadIdx.x & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave % KS, nw = wave / KS;
     const int tiles = (a.n + 15) / 16, steps = a.k / 128;
-    const int tile = blockIdx.x * (kW4Threads / 64) + (threadIdx.x >> 6);
-    if (tile >= tiles) return;
-    if (static_cast<uint32_t>(a.scalars[EP_SCALAR_ERROR_BITS]) & EP_ERRBIT_FATAL) return;
-    int start, rows;
-    const int e = active_expert(a.counts, a.psum, a.num_experts, blockIdx.y, lane, &start, &rows);
-    if (e < 0) return;
-    constexpr int kPer = 128 / GROUP;
-    const int64_t record = (static_cast<int64_t>(e) * tiles + tile) * steps;
-    const u32x4 *codes = static_cast<const u32x4 *>(a.codes) + record * 64 + lane;
-    const char *scales = static_cast<const char *>(a.scales) +
-                         (record * 16 + (lane & 15)) * kPer * (FMT == EP_W4_INT4 ? 2 : 1);
-    const int out_col = tile * 16 + (lane & 15);
-    for (int m0 = 0; m0 < rows; m0 += 16) {
-        const int m = m0 + (lane & 15) < rows ? m0 + (lane & 15) : rows - 1;
-        const int64_t row = start + m;
-        const int64_t src = a.token_rows ? a.src_meta[row] / a.num_topk : row;
-        const char *x = static_cast<const char *>(a.x) + (src * a.k + 8 * q) * (FP8 ? 1 : 2);
-        f32x4 total = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < steps; ++s) {
-            const u32x4 w = codes[static_cast<int64_t>(s) * 64];
-            u32x4 xs[4];
+    const int tile0 = (blockIdx.x * NW + nw) * NT;
+    const uint32_t bits = static_cast<uint32_t>(a.scalars[EP_SCALAR_ERROR_BITS]);
+    uint32_t mask = 0x000F000Fu, one28 = 0x43004300u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(one28));
+
+    for (int number = blockIdx.y; number < passes; number += gridDim.y) {
+        const Pass pass = find_pass(a.counts, a.psum, a.num_experts, number, 16 * MT, lane);
+        if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
+        // The group's records are consecutive; tiles behind the last are read as the
+        // last and not stored.
+        constexpr int kScaleStep = MX ? 64 : 32 * P;                     // bytes of a record's scales
+        const int first = tile0 < tiles ? tile0 : tiles - 1;
+        const int mine = first + NT <= tiles ? NT : tiles - first;
+        const int64_t record = (static_cast<int64_t>(pass.expert) * tiles + first) * steps;
+        const Buffer codes = bounded(static_cast<const char *>(a.codes) + record * 1024,
+                                     mine * steps * 1024);
+        const Buffer scales = bounded(static_cast<const char *>(a.scales) + record * kScaleStep,
+                                      mine * steps * kScaleStep);
+        const uint32_t code_at = 16 * lane;
+        const uint32_t scale_at = MX ? lane : 8 * P * q;
+        const int rounds = (steps + KS - 1) / KS;
+        auto step = [&](int round) { return round * KS + kg; };
+        auto held = [&](int s) { return s < steps ? s : steps - 1; };
+        // rounds behind the last one read nothing
+        auto load_w = [&](R &r, int round) {
+            const uint32_t cat = round < rounds ? code_at : kNowhere;
+            const uint32_t sat0 = round < rounds ? scale_at : kNowhere;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (FP8) xs[j] = e4m3_bf16(*reinterpret_cast<const u32x2 *>(x + s * 128 + 32 * j));
-                else xs[j] = *reinterpret_cast<const u32x4 *>(x + (s * 128 + 32 * j) * 2);
-            }
-            f32x4 part = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (FMT == EP_W4_MXFP4) {
-                const uint32_t sc = *reinterpret_cast<const uint32_t *>(scales + s * 64);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    part = mfma(xs[j], mxfp4(w[j], (sc >> (8 * j)) & 0xFFu), part);
-            } else {
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(scales + s * 32 * kPer);
-#pragma unroll
-                for (int g = 0; g < kPer; ++g) {
-                    f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int j = g * 4 / kPer; j < (g + 1) * 4 / kPer; ++j) {
-                        acc = mfma(xs[j], u32x4{kMinus136, kMinus136, kMinus136, kMinus136}, acc);
-                        acc = mfma(xs[j], int4_plus128(w[j]), acc);
-                    }
-                    const float f = __uint_as_float(static_cast<uint32_t>(sc[g]) << 16);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) part[i] = __builtin_fmaf(f, acc[i], part[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (FP8) {
-                    const int mi = m0 + 4 * q + i;
-                    const int64_t ri = start + (mi < rows ? mi : rows - 1);
-                    const int64_t si = a.token_rows ? a.src_meta[ri] / a.num_topk : ri;
-                    total[i] = __builtin_fmaf(
-                        load_scale(a.sf.p, a.sf.ts, a.sf.hs, si, s, a.sf.ue8m0), part[i], total[i]);
+            for (int t = 0; t < NT; ++t) {
+                const int at = (t < mine ? t : 0) * steps + held(step(round));
+                r.w[t] = __builtin_amdgcn_raw_buffer_load_b128(codes, cat, at * 1024, kStream);
+                const int sat = at * kScaleStep;
+                if (MX) {
+                    r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b8(scales, sat0, sat, 0);
+                } else if (P == 1) {
+                    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, sat0, sat, 0);
+                    r.sw[t][0] = v.x;
+                    r.sw[t][1 % R::kScaleWords] = v.y;
                 } else {
-                    total[i] += part[i];
+#pragma unroll
+                    for (int i = 0; i < R::kScaleWords / 4; ++i) {
+                        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(scales, sat0 + 16 * i,
+                                                                              sat, 0);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) r.sw[t][(4 * i + k) % R::kScaleWords] = v[k];
+                    }
                 }
             }
+        };
+        // the weights of the first rounds are on their way before anything of x is known
+        R w[D];
+#pragma unroll
+        for (int d = 0; d + 1 < D; ++d) load_w(w[d], d);
+        // Unit i = t * U + j of a step's x, and the scales of tile i, are brought by wave
+        // i % NW (by several, the same values, where there are fewer units than waves).
+        const char *xp[PER];
+        const uint32_t *sp[SPER];
+        auto source = [&](int t) {
+            const int m = 16 * t + (lane & 15);
+            const int64_t row = pass.start + (m < pass.rows ? m : pass.rows - 1);
+            return a.token_rows ? static_cast<int64_t>(a.src_meta[row] / a.num_topk) : row;
+        };
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int i = (p * NW + nw) % F, j = i % U;
+            const int ch = DIRECT ? 64 * j + 16 * q : first_channel(!MX, j, q);
+            xp[p] = static_cast<const char *>(a.x) +
+                    (source(i / U) * a.k + ch) * (FP8 ? 1 : 2);
+        }
+        if (FP8) {
+#pragma unroll
+            for (int p = 0; p < SPER; ++p) {
+                const int i = (p * NW + nw) % MT;
+                sp[p] = a.sf.p + source(i) * a.sf.ts;
+            }
+        }
+        struct X {
+            u32x4 v[PER];
+            float sf[SPER];
+        };
+        auto load_x = [&](X &r, int round) {
+#pragma unroll
+            for (int p = 0; p < PER; ++p) {
+                const char *x = xp[p] + held(step(round)) * (FP8 ? 128 : 256);
+                if (FP8 && !DIRECT) {
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(x);
+                    r.v[p].x = v.x;
+                    r.v[p].y = v.y;
+                } else {
+                    r.v[p] = *reinterpret_cast<const u32x4 *>(x);
+                }
+            }
+            if (FP8) {
+#pragma unroll
+                for (int p = 0; p < SPER; ++p)
+                    r.sf[p] = load_scale(sp[p], 0, a.sf.hs, 0, held(step(round)), a.sf.ue8m0);
+            }
+        };
+        // Steps behind the last count as zeros.
+        auto store_x = [&](const X &r, int round, int half) {
+            const int buf = half * KS + kg;
+#pragma unroll
+            for (int p = 0; p < PER; ++p) {
+                const uint32_t keep = step(round) < steps ? 0xFFFFFFFFu : 0u;
+                const u32x4 v = FP8 && !DIRECT ? e4m3_bf16(u32x2{r.v[p].x, r.v[p].y}) : r.v[p];
+                lds[(buf * F + (p * NW + nw) % F) * 64 + lane] = v & keep;
+            }
+            if (FP8) {
+#pragma unroll
+                for (int p = 0; p < SPER; ++p)
+                    lds_sf[(buf * MT + (p * NW + nw) % MT) * 16 + (lane & 15)] =
+                        step(round) < steps ? r.sf[p] : 0.0f;
+            }
+        };
+        f32x4 total[MT][NT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) total[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto compute = [&](const R &r, int half) {
+            const u32x4 *xl = lds + (half * KS + kg) * F * 64 + lane;
+            float sx[MT];
+            if (FP8)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    sx[t] = lds_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)];
+#pragma unroll
+            for (int g = 0; g < P; ++g) {
+                constexpr int J = U / P;
+                f32x4 acc[MT][NT];
+                u32x4 xs[MT][J];
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int j = 0; j < J; ++j) xs[t][j] = xl[(t * U + g * J + j) * 64];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    f32x4 from = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (!MX)
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            from = mfma(u32x4{kMinus136, kMinus136, kMinus136, kMinus136},
+                                        xs[t][j], from);
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) acc[t][u] = MX && !FP8 ? total[t][u] : from;
+                }
+                if (DIRECT) {
+#pragma unroll
+                    for (int u = 0; u < NT; ++u)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+                            acc[t][u] = mfma_mx(r.w[u], r.sw[u][0], xs[t][0],
+                                                xs[t][1 % J], acc[t][u]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int u = 0; u < NT; ++u) {
+                            const uint32_t w4 = r.w[u][(g * J + j) % 4];
+                            const u32x4 w = MX ? mxfp4(w4, r.sw[u][0])
+                                               : int4_plus128(w4, mask, one28);
+#pragma unroll
+                            for (int t = 0; t < MT; ++t)
+                                acc[t][u] = mfma(w, xs[t][j], acc[t][u]);
+                        }
+                }
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float f = 1.0f;
+                        if (!MX) {
+                            const uint32_t sw = r.sw[u][(i * P + g) / 2 % R::kScaleWords];
+                            f = (i * P + g) & 1 ? bf16_hi(sw) : bf16_lo(sw);
+                        }
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            if (MX && !FP8) {
+                                total[t][u][i] = acc[t][u][i];
+                                continue;
+                            }
+                            const float m = MX ? sx[t] : FP8 ? f * sx[t] : f;
+                            total[t][u][i] = __builtin_fmaf(m, acc[t][u][i], total[t][u][i]);
+                        }
+                    }
+            }
+        };
+        // While a round is computed on, the weights of the next D - 1 are on their way
+        // into registers, and their x into registers and then LDS.
+        X x[D];
+#pragma unroll
+        for (int d = 0; d + 1 < D; ++d) load_x(x[d], d);
+        store_x(x[0], 0, 0);
+        lds_barrier();
+        for (int round = 0; round < rounds;) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                load_x(x[(d + D - 1) % D], round + D - 1);
+                load_w(w[(d + D - 1) % D], round + D - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                compute(w[d], d);
+                __builtin_amdgcn_sched_barrier(0);
+                store_x(x[(d + 1) % D], round + 1, (d + 1) % D);
+                lds_barrier();
+                if (++round == rounds) break;
+            }
+        }
+        if (KS > 1) {
+            lds_barrier();                       // x is read: its room becomes the sums'
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+                    lds[((wave * MT + t) * NT + u) * 64 + lane] =
+                        __builtin_bit_cast(u32x4, total[t][u]);
+            lds_barrier();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int mi = m0 + 4 * q + i;
-            if (mi < rows && out_col < a.n)
-                static_cast<uint16_t *>(a.out)[static_cast<int64_t>(start + mi) * a.n + out_col] =
-                    static_cast<uint16_t>(pack2(total[i], 0.0f));
-        }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                if ((t * NT + u) % KS != kg) continue;
+                f32x4 v = total[t][u];
+                if (KS > 1) {
+                    v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        v += __builtin_bit_cast(
+                            f32x4, lds[(((nw * KS + k) * MT + t) * NT + u) * 64 + lane]);
+                }
+                const int m = 16 * t + (lane & 15), col = (tile0 + u) * 16 + 4 * q;
+                if (m < pass.rows && col < a.n)
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) +
+                                               static_cast<int64_t>(pass.start + m) * a.n + col) =
+                        u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+            }
+        if (number + gridDim.y < passes) lds_barrier();      // the sums are read
     }
 }
 
-template <int FMT, int GROUP>
-hipError_t launch_w4(const W4Args &a, hipStream_t stream) {
-    const int tiles = (a.n + 15) / 16;
-    const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk;
-    const int active = static_cast<int>(slots < a.num_experts ? slots : a.num_experts);
-    const dim3 grid((tiles + 3) / 4, active), block(kW4Threads);
-    if (a.x_fp8) w4_kernel<FMT, GROUP, true><<<grid, block, 0, stream>>>(a);
-    else w4_kernel<FMT, GROUP, false><<<grid, block, 0, stream>>>(a);
+template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
+hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t stream) {
+    constexpr int per_block = NT * (kW4Waves / KS);
+    const int groups = ((a.n + 15) / 16 + per_block - 1) / per_block;
+    // no more passes than these: every expert's last one may be partly filled
+    const int64_t passes = active + slots / (16 * MT);
+    // a launch holds fewer than 2^32 threads, and 2^16 blocks along y
+    int64_t most = (int64_t(1) << 23) / groups;
+    most = most < 1 ? 1 : most > 32768 ? 32768 : most;
+    const dim3 grid(groups, static_cast<uint32_t>(passes < most ? passes : most));
+    w4_kernel<FMT, GROUP, FP8, NT, MT, KS, D><<<grid, kW4Threads, 0, stream>>>(
+        a, static_cast<int>(passes));
     return hipGetLastError();
+}
+
+// Tile and split, by the sizes that the host knows.
+//   Rows a pass: 16 up to 12 rows an expert on average, 32 beyond.  At 16 rows an expert
+//   (64 experts, 4096 x 7168) 32 take 193 us and 16 take 225 with EP_W4_INT4, 165 and 215
+//   with EP_W4_MXFP4, whose second passes re-read the weights; at 8 rows an expert 195 and 161, and
+//   160 and 159, as half of the wider tile is empty.  64 rows a pass gave nothing
+//   (64 rows an expert: 150 us against 135).
+//   Outputs a wave and waves a group: the widest that leaves 384 blocks, one and a
+//   half a compute unit.  One token of 8 experts (4096 x 7168, 2048 tiles): 24.0 us
+//   with two waves a group of 32 outputs, 30.3 with one, 47.0 with 64 outputs a wave;
+//   26 experts with rows: 73.9, 74.7 and 71.4; 2 experts of 1024 outputs: 8.5 with
+//   four waves a group, 10.8 with two.  Three rounds in registers instead of two where a wave
+//   has 32 outputs of 16 rows (25.7 -> 23.9 us): more of the weights is in flight.
+template <int FMT, int GROUP, bool FP8>
+hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
+    const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk;
+    const int64_t active = slots < a.num_experts ? slots : a.num_experts;
+    const int64_t tiles = active * ((a.n + 15) / 16);
+    const bool wide = slots > 12 * static_cast<int64_t>(a.num_experts);
+    constexpr int64_t kBlocks = 384;
+    if (tiles >= 16 * kBlocks)
+        return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, 2>(a, active, slots, stream)
+                    : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);
+    if (tiles >= 8 * kBlocks)
+        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
+                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 3>(a, active, slots, stream);
+    if (tiles >= 4 * kBlocks)
+        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 2, 2>(a, active, slots, stream)
+                    : launch_w4<FMT, GROUP, FP8, 2, 1, 2, 3>(a, active, slots, stream);
+    return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 4, 2>(a, active, slots, stream)
+                : launch_w4<FMT, GROUP, FP8, 2, 1, 4, 3>(a, active, slots, stream);
+}
+
+template <int FMT, int GROUP>
+hipError_t choose_x(const W4Args &a, hipStream_t stream) {
+    return a.x_fp8 ? choose_w4<FMT, GROUP, true>(a, stream)
+                   : choose_w4<FMT, GROUP, false>(a, stream);
 }
 
 }  // namespace
@@ -241,10 +553,10 @@ hipError_t launch_w4_pack(const void *codes, const void *scales, int32_t num_exp
 }
 
 hipError_t launch_expert_w4(const W4Args &a, hipStream_t stream) {
-    if (a.fmt == EP_W4_MXFP4) return launch_w4<EP_W4_MXFP4, 32>(a, stream);
-    if (a.group == 32) return launch_w4<EP_W4_INT4, 32>(a, stream);
-    if (a.group == 64) return launch_w4<EP_W4_INT4, 64>(a, stream);
-    return launch_w4<EP_W4_INT4, 128>(a, stream);
+    if (a.fmt == EP_W4_MXFP4) return choose_x<EP_W4_MXFP4, 32>(a, stream);
+    if (a.group == 32) return choose_x<EP_W4_INT4, 32>(a, stream);
+    if (a.group == 64) return choose_x<EP_W4_INT4, 64>(a, stream);
+    return choose_x<EP_W4_INT4, 128>(a, stream);
 }
 
 }  // namespace ep

@@ -221,7 +221,7 @@ constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
 //   The weights of the next D - 1 rounds stay in flight across the rounds'
 //   barriers, which order LDS only.
 template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
-__global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int passes) {
+__global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int first_pass) {
     typedef Records<FMT, GROUP, NT> R;
     constexpr bool MX = FMT == EP_W4_MXFP4;
     constexpr bool DIRECT = MX && FP8;           // codes go to the matrix instruction as they are
@@ -245,239 +245,239 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int p
     asm("" : "+s"(mask));
     asm("" : "+v"(one28));
 
-    for (int number = blockIdx.y; number < passes; number += gridDim.y) {
-        const Pass pass = find_pass(a.counts, a.psum, a.num_experts, number, 16 * MT, lane);
-        if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
-        // The group's records are consecutive; tiles behind the last are read as the
-        // last and not stored.
-        constexpr int kScaleStep = MX ? 64 : 32 * P;                     // bytes of a record's scales
-        const int first = tile0 < tiles ? tile0 : tiles - 1;
-        const int mine = first + NT <= tiles ? NT : tiles - first;
-        const int64_t record = (static_cast<int64_t>(pass.expert) * tiles + first) * steps;
-        const Buffer codes = bounded(static_cast<const char *>(a.codes) + record * 1024,
-                                     mine * steps * 1024);
-        const Buffer scales = bounded(static_cast<const char *>(a.scales) + record * kScaleStep,
-                                      mine * steps * kScaleStep);
-        const uint32_t code_at = 16 * lane;
-        const uint32_t scale_at = MX ? lane : 8 * P * q;
-        const int rounds = (steps + KS - 1) / KS;
-        auto step = [&](int round) { return round * KS + kg; };
-        auto held = [&](int s) { return s < steps ? s : steps - 1; };
-        // rounds behind the last one read nothing
-        auto load_w = [&](R &r, int round) {
-            const uint32_t cat = round < rounds ? code_at : kNowhere;
-            const uint32_t sat0 = round < rounds ? scale_at : kNowhere;
+    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, 16 * MT,
+                                lane);
+    if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
+    // The group's records are consecutive; tiles behind the last are read as the
+    // last and not stored.
+    constexpr int kScaleStep = MX ? 64 : 32 * P;                     // bytes of a record's scales
+    const int first = tile0 < tiles ? tile0 : tiles - 1;
+    const int mine = first + NT <= tiles ? NT : tiles - first;
+    const int64_t record = (static_cast<int64_t>(pass.expert) * tiles + first) * steps;
+    const Buffer codes = bounded(static_cast<const char *>(a.codes) + record * 1024,
+                                 mine * steps * 1024);
+    const Buffer scales = bounded(static_cast<const char *>(a.scales) + record * kScaleStep,
+                                  mine * steps * kScaleStep);
+    uint32_t code_at = 16 * lane;
+    uint32_t scale_at = MX ? lane : 8 * P * q;
+    const int rounds = (steps + KS - 1) / KS;
+    auto step = [&](int round) { return round * KS + kg; };
+    auto held = [&](int s) { return s < steps ? s : steps - 1; };
+    // Called for one round after the other: offsets and pointers are moved on in
+    // place, as an address in a register of its own would be put where an
+    // older load is still to arrive, and wait for it.  Rounds behind the last read nothing.
+    auto load_w = [&](R &r, int round) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int at = (t < mine ? t : 0) * steps + held(step(round));
-                r.w[t] = __builtin_amdgcn_raw_buffer_load_b128(codes, cat, at * 1024, kStream);
-                const int sat = at * kScaleStep;
-                if (MX) {
-                    r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b8(scales, sat0, sat, 0);
-                } else if (P == 1) {
-                    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, sat0, sat, 0);
-                    r.sw[t][0] = v.x;
-                    r.sw[t][1 % R::kScaleWords] = v.y;
-                } else {
+        for (int t = 0; t < NT; ++t) {
+            const int at = (t < mine ? t : 0) * steps + held(step(round));
+            r.w[t] = __builtin_amdgcn_raw_buffer_load_b128(codes, code_at, at * 1024, kStream);
+            const int sat = at * kScaleStep;
+            if (MX) {
+                r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b8(scales, scale_at, sat, 0);
+            } else if (P == 1) {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, scale_at, sat, 0);
+                r.sw[t][0] = v.x;
+                r.sw[t][1 % R::kScaleWords] = v.y;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < R::kScaleWords / 4; ++i) {
-                        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(scales, sat0 + 16 * i,
-                                                                              sat, 0);
+                for (int i = 0; i < R::kScaleWords / 4; ++i) {
+                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+                        scales, scale_at + 16 * i, sat, 0);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) r.sw[t][(4 * i + k) % R::kScaleWords] = v[k];
-                    }
+                    for (int k = 0; k < 4; ++k) r.sw[t][(4 * i + k) % R::kScaleWords] = v[k];
                 }
             }
-        };
-        // the weights of the first rounds are on their way before anything of x is known
-        R w[D];
+        }
+        if (round + 1 >= rounds) code_at = scale_at = kNowhere;
+    };
+    // the weights of the first rounds are on their way before anything of x is known
+    R w[D];
 #pragma unroll
-        for (int d = 0; d + 1 < D; ++d) load_w(w[d], d);
-        // Unit i = t * U + j of a step's x, and the scales of tile i, are brought by wave
-        // i % NW (by several, the same values, where there are fewer units than waves).
-        const char *xp[PER];
-        const uint32_t *sp[SPER];
-        auto source = [&](int t) {
-            const int m = 16 * t + (lane & 15);
-            const int64_t row = pass.start + (m < pass.rows ? m : pass.rows - 1);
-            return a.token_rows ? static_cast<int64_t>(a.src_meta[row] / a.num_topk) : row;
-        };
+    for (int d = 0; d + 1 < D; ++d) load_w(w[d], d);
+    // Unit i = t * U + j of a step's x, and the scales of tile i, are brought by wave
+    // i % NW (by several, the same values, where there are fewer units than waves).
+    const char *xp[PER];
+    const uint32_t *sp[SPER];
+    auto source = [&](int t) {
+        const int m = 16 * t + (lane & 15);
+        const int64_t row = pass.start + (m < pass.rows ? m : pass.rows - 1);
+        return a.token_rows ? static_cast<int64_t>(a.src_meta[row] / a.num_topk) : row;
+    };
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int i = (p * NW + nw) % F, j = i % U;
+        const int ch = DIRECT ? 64 * j + 16 * q : first_channel(!MX, j, q);
+        xp[p] = static_cast<const char *>(a.x) +
+                (source(i / U) * a.k + held(kg) * 128 + ch) * (FP8 ? 1 : 2);
+    }
+    if (FP8) {
+#pragma unroll
+        for (int p = 0; p < SPER; ++p) {
+            const int i = (p * NW + nw) % MT;
+            sp[p] = a.sf.p + source(i) * a.sf.ts;
+        }
+    }
+    struct X {
+        u32x4 v[PER];
+        float sf[SPER];
+    };
+    auto load_x = [&](X &r, int round) {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int i = (p * NW + nw) % F, j = i % U;
-            const int ch = DIRECT ? 64 * j + 16 * q : first_channel(!MX, j, q);
-            xp[p] = static_cast<const char *>(a.x) +
-                    (source(i / U) * a.k + ch) * (FP8 ? 1 : 2);
+            if (FP8 && !DIRECT) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(xp[p]);
+                r.v[p].x = v.x;
+                r.v[p].y = v.y;
+            } else {
+                r.v[p] = *reinterpret_cast<const u32x4 *>(xp[p]);
+            }
+            // the row's last step stays the last
+            xp[p] += step(round + 1) < steps ? KS * 128 * (FP8 ? 1 : 2) : 0;
         }
         if (FP8) {
 #pragma unroll
-            for (int p = 0; p < SPER; ++p) {
-                const int i = (p * NW + nw) % MT;
-                sp[p] = a.sf.p + source(i) * a.sf.ts;
-            }
+            for (int p = 0; p < SPER; ++p)
+                r.sf[p] = load_scale(sp[p], 0, a.sf.hs, 0, held(step(round)), a.sf.ue8m0);
         }
-        struct X {
-            u32x4 v[PER];
-            float sf[SPER];
-        };
-        auto load_x = [&](X &r, int round) {
+    };
+    // Steps behind the last count as zeros.
+    auto store_x = [&](const X &r, int round, int half) {
+        const int buf = half * KS + kg;
 #pragma unroll
-            for (int p = 0; p < PER; ++p) {
-                const char *x = xp[p] + held(step(round)) * (FP8 ? 128 : 256);
-                if (FP8 && !DIRECT) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(x);
-                    r.v[p].x = v.x;
-                    r.v[p].y = v.y;
-                } else {
-                    r.v[p] = *reinterpret_cast<const u32x4 *>(x);
-                }
-            }
-            if (FP8) {
-#pragma unroll
-                for (int p = 0; p < SPER; ++p)
-                    r.sf[p] = load_scale(sp[p], 0, a.sf.hs, 0, held(step(round)), a.sf.ue8m0);
-            }
-        };
-        // Steps behind the last count as zeros.
-        auto store_x = [&](const X &r, int round, int half) {
-            const int buf = half * KS + kg;
-#pragma unroll
-            for (int p = 0; p < PER; ++p) {
-                const uint32_t keep = step(round) < steps ? 0xFFFFFFFFu : 0u;
-                const u32x4 v = FP8 && !DIRECT ? e4m3_bf16(u32x2{r.v[p].x, r.v[p].y}) : r.v[p];
-                lds[(buf * F + (p * NW + nw) % F) * 64 + lane] = v & keep;
-            }
-            if (FP8) {
-#pragma unroll
-                for (int p = 0; p < SPER; ++p)
-                    lds_sf[(buf * MT + (p * NW + nw) % MT) * 16 + (lane & 15)] =
-                        step(round) < steps ? r.sf[p] : 0.0f;
-            }
-        };
-        f32x4 total[MT][NT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int u = 0; u < NT; ++u) total[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        auto compute = [&](const R &r, int half) {
-            const u32x4 *xl = lds + (half * KS + kg) * F * 64 + lane;
-            float sx[MT];
-            if (FP8)
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    sx[t] = lds_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)];
-#pragma unroll
-            for (int g = 0; g < P; ++g) {
-                constexpr int J = U / P;
-                f32x4 acc[MT][NT];
-                u32x4 xs[MT][J];
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int j = 0; j < J; ++j) xs[t][j] = xl[(t * U + g * J + j) * 64];
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    f32x4 from = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    if (!MX)
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            from = mfma(u32x4{kMinus136, kMinus136, kMinus136, kMinus136},
-                                        xs[t][j], from);
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) acc[t][u] = MX && !FP8 ? total[t][u] : from;
-                }
-                if (DIRECT) {
-#pragma unroll
-                    for (int u = 0; u < NT; ++u)
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-                            acc[t][u] = mfma_mx(r.w[u], r.sw[u][0], xs[t][0],
-                                                xs[t][1 % J], acc[t][u]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int u = 0; u < NT; ++u) {
-                            const uint32_t w4 = r.w[u][(g * J + j) % 4];
-                            const u32x4 w = MX ? mxfp4(w4, r.sw[u][0])
-                                               : int4_plus128(w4, mask, one28);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t)
-                                acc[t][u] = mfma(w, xs[t][j], acc[t][u]);
-                        }
-                }
-#pragma unroll
-                for (int u = 0; u < NT; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f = 1.0f;
-                        if (!MX) {
-                            const uint32_t sw = r.sw[u][(i * P + g) / 2 % R::kScaleWords];
-                            f = (i * P + g) & 1 ? bf16_hi(sw) : bf16_lo(sw);
-                        }
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            if (MX && !FP8) {
-                                total[t][u][i] = acc[t][u][i];
-                                continue;
-                            }
-                            const float m = MX ? sx[t] : FP8 ? f * sx[t] : f;
-                            total[t][u][i] = __builtin_fmaf(m, acc[t][u][i], total[t][u][i]);
-                        }
-                    }
-            }
-        };
-        // While a round is computed on, the weights of the next D - 1 are on their way
-        // into registers, and their x into registers and then LDS.
-        X x[D];
-#pragma unroll
-        for (int d = 0; d + 1 < D; ++d) load_x(x[d], d);
-        store_x(x[0], 0, 0);
-        lds_barrier();
-        for (int round = 0; round < rounds;) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                load_x(x[(d + D - 1) % D], round + D - 1);
-                load_w(w[(d + D - 1) % D], round + D - 1);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(w[d], d);
-                __builtin_amdgcn_sched_barrier(0);
-                store_x(x[(d + 1) % D], round + 1, (d + 1) % D);
-                lds_barrier();
-                if (++round == rounds) break;
-            }
+        for (int p = 0; p < PER; ++p) {
+            const uint32_t keep = step(round) < steps ? 0xFFFFFFFFu : 0u;
+            const u32x4 v = FP8 && !DIRECT ? e4m3_bf16(u32x2{r.v[p].x, r.v[p].y}) : r.v[p];
+            lds[(buf * F + (p * NW + nw) % F) * 64 + lane] = v & keep;
         }
-        if (KS > 1) {
-            lds_barrier();                       // x is read: its room becomes the sums'
+        if (FP8) {
+#pragma unroll
+            for (int p = 0; p < SPER; ++p)
+                lds_sf[(buf * MT + (p * NW + nw) % MT) * 16 + (lane & 15)] =
+                    step(round) < steps ? r.sf[p] : 0.0f;
+        }
+    };
+    f32x4 total[MT][NT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) total[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](const R &r, int half) {
+        const u32x4 *xl = lds + (half * KS + kg) * F * 64 + lane;
+        float sx[MT];
+        if (FP8)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                sx[t] = lds_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)];
+#pragma unroll
+        for (int g = 0; g < P; ++g) {
+            constexpr int J = U / P;
+            f32x4 acc[MT][NT];
+            u32x4 xs[MT][J];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
+                for (int j = 0; j < J; ++j) xs[t][j] = xl[(t * U + g * J + j) * 64];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                f32x4 from = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (!MX)
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        from = mfma(u32x4{kMinus136, kMinus136, kMinus136, kMinus136},
+                                    xs[t][j], from);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) acc[t][u] = MX && !FP8 ? total[t][u] : from;
+            }
+            if (DIRECT) {
+#pragma unroll
                 for (int u = 0; u < NT; ++u)
-                    lds[((wave * MT + t) * NT + u) * 64 + lane] =
-                        __builtin_bit_cast(u32x4, total[t][u]);
-            lds_barrier();
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        acc[t][u] = mfma_mx(r.w[u], r.sw[u][0], xs[t][0],
+                                            xs[t][1 % J], acc[t][u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        const uint32_t w4 = r.w[u][(g * J + j) % 4];
+                        const u32x4 w = MX ? mxfp4(w4, r.sw[u][0])
+                                           : int4_plus128(w4, mask, one28);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+                            acc[t][u] = mfma(w, xs[t][j], acc[t][u]);
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f = 1.0f;
+                    if (!MX) {
+                        const uint32_t sw = r.sw[u][(i * P + g) / 2 % R::kScaleWords];
+                        f = (i * P + g) & 1 ? bf16_hi(sw) : bf16_lo(sw);
+                    }
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        if (MX && !FP8) {
+                            total[t][u][i] = acc[t][u][i];
+                            continue;
+                        }
+                        const float m = MX ? sx[t] : FP8 ? f * sx[t] : f;
+                        total[t][u][i] = __builtin_fmaf(m, acc[t][u][i], total[t][u][i]);
+                    }
+                }
         }
+    };
+    // While a round is computed on, the weights of the next D - 1 are on their way
+    // into registers, and their x into registers and then LDS.
+    X x[D];
+#pragma unroll
+    for (int d = 0; d + 1 < D; ++d) load_x(x[d], d);
+    store_x(x[0], 0, 0);
+    lds_barrier();
+    for (int round = 0; round < rounds;) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_x(x[(d + D - 1) % D], round + D - 1);
+            load_w(w[(d + D - 1) % D], round + D - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(w[d], d);
+            __builtin_amdgcn_sched_barrier(0);
+            store_x(x[(d + 1) % D], round + 1, (d + 1) % D);
+            lds_barrier();
+            if (++round == rounds) break;
+        }
+    }
+    if (KS > 1) {
+        lds_barrier();                       // x is read: its room becomes the sums'
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                if ((t * NT + u) % KS != kg) continue;
-                f32x4 v = total[t][u];
-                if (KS > 1) {
-                    v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        v += __builtin_bit_cast(
-                            f32x4, lds[(((nw * KS + k) * MT + t) * NT + u) * 64 + lane]);
-                }
-                const int m = 16 * t + (lane & 15), col = (tile0 + u) * 16 + 4 * q;
-                if (m < pass.rows && col < a.n)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) +
-                                               static_cast<int64_t>(pass.start + m) * a.n + col) =
-                        u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-            }
-        if (number + gridDim.y < passes) lds_barrier();      // the sums are read
+            for (int u = 0; u < NT; ++u)
+                lds[((wave * MT + t) * NT + u) * 64 + lane] =
+                    __builtin_bit_cast(u32x4, total[t][u]);
+        lds_barrier();
     }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            if ((t * NT + u) % KS != kg) continue;
+            f32x4 v = total[t][u];
+            if (KS > 1) {
+                v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    v += __builtin_bit_cast(
+                        f32x4, lds[(((nw * KS + k) * MT + t) * NT + u) * 64 + lane]);
+            }
+            const int m = 16 * t + (lane & 15), col = (tile0 + u) * 16 + 4 * q;
+            if (m < pass.rows && col < a.n)
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) +
+                                           static_cast<int64_t>(pass.start + m) * a.n + col) =
+                    u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+        }
 }
 
 template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
@@ -489,37 +489,47 @@ hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t
     // a launch holds fewer than 2^32 threads, and 2^16 blocks along y
     int64_t most = (int64_t(1) << 23) / groups;
     most = most < 1 ? 1 : most > 32768 ? 32768 : most;
-    const dim3 grid(groups, static_cast<uint32_t>(passes < most ? passes : most));
-    w4_kernel<FMT, GROUP, FP8, NT, MT, KS, D><<<grid, kW4Threads, 0, stream>>>(
-        a, static_cast<int>(passes));
-    return hipGetLastError();
+    for (int64_t p = 0; p < passes; p += most) {
+        const dim3 grid(groups, static_cast<uint32_t>(passes - p < most ? passes - p : most));
+        w4_kernel<FMT, GROUP, FP8, NT, MT, KS, D><<<grid, kW4Threads, 0, stream>>>(
+            a, static_cast<int>(p));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
-// Tile and split, by the sizes that the host knows.
-//   Rows a pass: 16 up to 12 rows an expert on average, 32 beyond.  At 16 rows an expert
-//   (64 experts, 4096 x 7168) 32 take 193 us and 16 take 225 with EP_W4_INT4, 165 and 215
-//   with EP_W4_MXFP4, whose second passes re-read the weights; at 8 rows an expert 195 and 161, and
-//   160 and 159, as half of the wider tile is empty.  64 rows a pass gave nothing
-//   (64 rows an expert: 150 us against 135).
+// Tile and split, by the sizes that the host knows (us at 64 experts unless said).
+//   Rows a pass: 16 or 32.  The codes' conversion and the weights' reading are paid once a
+//   pass, an empty half of a wide one costs its matrix instructions.  EP_W4_INT4,
+//   4096 x 7168: 161 (16) and 195 (32) at 8 rows an expert on average, 225 and 193 at 16; so
+//   32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4 rows, 215 and 165
+//   at 16; so 32 beyond 6.  64 rows gave nothing (16 experts of 64 rows: 150 against 135).
 //   Outputs a wave and waves a group: the widest that leaves 384 blocks, one and a
-//   half a compute unit.  One token of 8 experts (4096 x 7168, 2048 tiles): 24.0 us
+//   half a compute unit.  One token of 8 experts (4096 x 7168, 2048 tiles): 24.0
 //   with two waves a group of 32 outputs, 30.3 with one, 47.0 with 64 outputs a wave;
 //   26 experts with rows: 73.9, 74.7 and 71.4; 2 experts of 1024 outputs: 8.5 with
-//   four waves a group, 10.8 with two.  Three rounds in registers instead of two where a wave
-//   has 32 outputs of 16 rows (25.7 -> 23.9 us): more of the weights is in flight.
+//   four waves a group, 10.8 with two.  Short rows leave a block little to do between
+//   its first and last loads, which more blocks a compute unit hide: 64 outputs a wave
+//   from 32 steps on only (7168 x 2048, 16 steps: 88 with 64, 81 with 32 outputs).
+//   Three steps in registers instead of two keep more of the weights in flight where a
+//   block is short of waves (one token: 25.7 -> 23.9) or a step is long (64 outputs of
+//   32 rows: 204 -> 197 at 16 rows an expert; not with groups of 32 or 64, whose scales
+//   leave too few registers: 249 -> 285).
 template <int FMT, int GROUP, bool FP8>
 hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk;
     const int64_t active = slots < a.num_experts ? slots : a.num_experts;
     const int64_t tiles = active * ((a.n + 15) / 16);
-    const bool wide = slots > 12 * static_cast<int64_t>(a.num_experts);
+    const bool wide = slots > (FMT == EP_W4_MXFP4 ? 6 : 12) * static_cast<int64_t>(a.num_experts);
     constexpr int64_t kBlocks = 384;
-    if (tiles >= 16 * kBlocks)
-        return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, 2>(a, active, slots, stream)
+    constexpr int deep = FMT == EP_W4_MXFP4 || GROUP == 128 ? 3 : 2;
+    if (tiles >= 16 * kBlocks && a.k >= 32 * 128)
+        return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, deep>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);
     if (tiles >= 8 * kBlocks)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
-                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 3>(a, active, slots, stream);
+                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
     if (tiles >= 4 * kBlocks)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 2, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 2, 1, 2, 3>(a, active, slots, stream);

@@ -372,8 +372,10 @@ def _need(cond: bool, msg: str):
 
 
 def _dev(t: torch.Tensor, name: str):
-    _need(t.is_cuda, f"{name} must be a device tensor")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _dev_strided(t: torch.Tensor, name: str):
@@ -488,23 +490,27 @@ _CODE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
 def _here(*tensors):
     """The calls enqueue on the current device's stream: every tensor must live there."""
+    current = None
     for t in tensors:
-        if t is not None and t.is_cuda:
-            _need(t.device.index == torch.cuda.current_device(),
-                  "tensors must be on the current device")
+        if t is not None:
+            d = t.get_device()
+            if d >= 0 and current is None:
+                current = torch.cuda.current_device()
+            if d >= 0 and d != current:
+                raise ValueError("tensors must be on the current device")
 
 
-def _rows_of(t, name, rows, cols, dtype):
-    """``t`` must be a contiguous device tensor [rows, cols]."""
+def _rows_of(t, name, shape, dtype):
+    """``t`` must be a contiguous device tensor of this shape and type."""
     _dev(t, name)
-    _need(t.dtype == dtype and tuple(t.shape) == (rows, cols),
-          f"{name} must be {dtype} [{rows}, {cols}]")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
 
 
 def _norm_weight(weight, hidden) -> int:
     _dev(weight, "weight")
-    _need(weight.dtype in (torch.bfloat16, torch.float32) and tuple(weight.shape) == (hidden,),
-          "weight must be bf16 or fp32 [H]")
+    if weight.shape != (hidden,) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight must be bf16 or fp32 [H]")
     return EP_BF16 if weight.dtype == torch.bfloat16 else EP_F32
 
 
@@ -515,15 +521,15 @@ def _add_rmsnorm_call(x, weight, residual, eps, out_z, out_y, want_y, scale_form
     T, H = x.shape
     wdt = _norm_weight(weight, H)
     if residual is not None:
-        _rows_of(residual, "residual", T, H, torch.bfloat16)
+        _rows_of(residual, "residual", x.shape, torch.bfloat16)
         if out_z is None:
             out_z = torch.empty_like(x)
     if out_z is not None:
-        _rows_of(out_z, "out_z", T, H, torch.bfloat16)
+        _rows_of(out_z, "out_z", x.shape, torch.bfloat16)
     if want_y and out_y is None:
         out_y = torch.empty_like(x)
     if out_y is not None:
-        _rows_of(out_y, "out_y", T, H, torch.bfloat16)
+        _rows_of(out_y, "out_y", x.shape, torch.bfloat16)
     fmt, ts, hs = EP_SF_F32, 0, 0
     if scale_format is not None:
         fmt = _sf_format(scale_format)
@@ -590,28 +596,27 @@ def add_rmsnorm_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Te
     _dev(z, "z")
     _need(z.dtype == torch.bfloat16 and z.dim() == 2, "z must be bf16 [T, H]")
     T, H = z.shape
-    _rows_of(grad_y, "grad_y", T, H, torch.bfloat16)
+    _rows_of(grad_y, "grad_y", z.shape, torch.bfloat16)
     wdt = _norm_weight(weight, H)
-    _dev(rstd, "rstd")
-    _need(rstd.dtype == torch.float32 and tuple(rstd.shape) == (T,), "rstd must be fp32 [T]")
+    _rows_of(rstd, "rstd", (T,), torch.float32)
     if grad_residual is not None:
-        _rows_of(grad_residual, "grad_residual", T, H, torch.bfloat16)
-    if want_grad_x and grad_x is None:
-        grad_x = torch.empty_like(z)
+        _rows_of(grad_residual, "grad_residual", z.shape, torch.bfloat16)
     if grad_x is not None:
-        _rows_of(grad_x, "grad_x", T, H, torch.bfloat16)
-    if want_grad_weight and grad_weight is None:
-        grad_weight = torch.empty(H, dtype=torch.float32, device=z.device)
+        _rows_of(grad_x, "grad_x", z.shape, torch.bfloat16)
+    elif want_grad_x:
+        grad_x = z.new_empty((T, H))
+    if grad_weight is not None:
+        _rows_of(grad_weight, "grad_weight", (H,), torch.float32)
+    elif want_grad_weight:
+        grad_weight = rstd.new_empty(H)
     nbytes = 0
     if grad_weight is not None:
-        _dev(grad_weight, "grad_weight")
-        _need(grad_weight.dtype == torch.float32 and tuple(grad_weight.shape) == (H,),
-              "grad_weight must be fp32 [H]")
         if workspace is None:
-            workspace = torch.empty(max(ep_add_rmsnorm_backward_workspace(T, H), 16),
-                                    dtype=torch.uint8, device=z.device)
-        _dev(workspace, "workspace")
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = ep_add_rmsnorm_backward_workspace(T, H)
+            workspace = rstd.new_empty(nbytes // 4)
+        else:
+            _dev(workspace, "workspace")
+            nbytes = workspace.numel() * workspace.element_size()
     _here(grad_y, z, weight, rstd, grad_residual, grad_x, grad_weight, workspace)
     _check(ep_add_rmsnorm_backward(_ptr(grad_y), _ptr(z), _ptr(weight), wdt, _ptr(rstd),
                                    _ptr(grad_residual), T, H, _ptr(grad_x), _ptr(grad_weight),
@@ -1187,7 +1192,7 @@ class Handle:
             _need(sf is None, "scale factors are for FP8 only")
         if out is None:
             out = torch.empty((self.capacity, weights.n), dtype=torch.bfloat16, device=x.device)
-        _rows_of(out, "out", self.capacity, weights.n, torch.bfloat16)
+        _rows_of(out, "out", (self.capacity, weights.n), torch.bfloat16)
         _here(x, sf, out, weights.codes, self.workspace)
         args = (ctypes.byref(self.h), _ptr(x), EP_FP8_E4M3 if fp8 else EP_BF16,
                 1 if token_rows else 0, weights.k, _ptr(sf), fmt, ts, hs, _ptr(weights.codes),
@@ -1203,8 +1208,8 @@ class Handle:
         _need(sf.dtype in _SF_DTYPES, f"{name} must be fp32 scales or int32 packs")
         fmt = EP_SF_F32 if sf.dtype == torch.float32 else EP_SF_UE8M0
         packs = ep_sf_packs(cols, fmt)
-        _need(packs > 0 and tuple(sf.shape) == (rows, packs),
-              f"{name} must be [{rows}, {packs}] for FP8 rows of {cols} channels")
+        if packs <= 0 or sf.shape != (rows, packs):
+            raise ValueError(f"{name} must be [{rows}, {packs}] for FP8 rows of {cols} channels")
         return (fmt, *sf.stride())
 
     def _row_weights(self, row_weights):
@@ -1249,7 +1254,7 @@ class Handle:
             _need(out_sf is None, "FP8 rows need a scale_format")
             if out is None:
                 out = torch.empty((cap, inter), dtype=torch.bfloat16, device=dev)
-            _rows_of(out, "out", cap, inter, torch.bfloat16)
+            _rows_of(out, "out", (cap, inter), torch.bfloat16)
         else:
             fmt = _sf_format(scale_format)
             packs = ep_sf_packs(inter, fmt)
@@ -1298,8 +1303,8 @@ class Handle:
         inter = grad_h.shape[1]
         _dev(saved, "saved")
         fp8 = saved.dtype in _CODE_DTYPES
-        _need((fp8 or saved.dtype == torch.bfloat16) and tuple(saved.shape) == (cap, 2 * inter),
-              f"saved must be bf16 or FP8 codes [{cap}, {2 * inter}]")
+        if saved.shape != (cap, 2 * inter) or not (fp8 or saved.dtype == torch.bfloat16):
+            raise ValueError(f"saved must be bf16 or FP8 codes [{cap}, {2 * inter}]")
         fmt, ts, hs = EP_SF_F32, 0, 0
         if fp8:
             _need(inter % 128 == 0, "inter must be a positive multiple of 128")
@@ -1310,7 +1315,7 @@ class Handle:
         if grad_gate_up is None:
             grad_gate_up = torch.empty((cap, 2 * inter), dtype=torch.bfloat16,
                                        device=grad_h.device)
-        _rows_of(grad_gate_up, "grad_gate_up", cap, 2 * inter, torch.bfloat16)
+        _rows_of(grad_gate_up, "grad_gate_up", (cap, 2 * inter), torch.bfloat16)
         if want_grad_weights and grad_row_weights is None:
             grad_row_weights = torch.empty(cap, dtype=torch.float32, device=grad_h.device)
         if grad_row_weights is not None:
@@ -1320,7 +1325,7 @@ class Handle:
         if want_h and out is None:
             out = torch.empty((cap, inter), dtype=torch.bfloat16, device=grad_h.device)
         if out is not None:
-            _rows_of(out, "out", cap, inter, torch.bfloat16)
+            _rows_of(out, "out", (cap, inter), torch.bfloat16)
         _here(grad_h, saved, saved_sf, row_weights, grad_gate_up, grad_row_weights, out,
               self.workspace)
         _check(ep_swiglu_backward(self.h, _ptr(grad_h), inter, _ptr(row_weights), _ptr(saved),

@@ -183,20 +183,33 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a) {
     }
 }
 
-// Sums of the blocks' rows: 16 lanes of 4 channels, 16 groups of rows a block.
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float *partial, int rows,
-                                                            int hidden, float *out) {
-    __shared__ f32x4 sums[16][16];
-    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-    const int c = (blockIdx.x * 16 + lane) * 4;
+// Sums of the blocks' rows, 32 channels a block: 8 lanes of 4 channels, 128 groups
+// that take every 128th row.  A group's loads are independent of each other, so
+// the kernel lasts a few memory latencies (8 groups of 64 loads in a chain took
+// 8 to 10 us for 512 rows of 7168).
+constexpr int kSumThreads = 1024;
+
+__global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float *partial, int rows,
+                                                                    int hidden, float *out) {
+    __shared__ f32x4 sums[kSumThreads / 64][8];
+    const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
+    const int c = (blockIdx.x * 8 + lane) * 4;
     f32x4 s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < hidden)
-        for (int r = group; r < rows; r += 16)
+    if (c < hidden) {
+#pragma unroll 4
+        for (int r = group; r < rows; r += kSumThreads / 8)
             s += *reinterpret_cast<const f32x4 *>(partial + static_cast<int64_t>(r) * hidden + c);
-    sums[group][lane] = s;
+    }
+#pragma unroll
+    for (int d = 8; d < 64; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += __shfl_xor(s[i], d);
+    if ((threadIdx.x & 63) < 8) sums[threadIdx.x >> 6][lane] = s;
     __syncthreads();
-    if (group != 0 || c >= hidden) return;
-    for (int g = 1; g < 16; ++g) s += sums[g][lane];
+    if (threadIdx.x >= 8 || c >= hidden) return;
+    s = sums[0][lane];
+#pragma unroll
+    for (int w = 1; w < kSumThreads / 64; ++w) s += sums[w][lane];
     *reinterpret_cast<f32x4 *>(out + c) = s;
 }
 
@@ -225,8 +238,8 @@ hipError_t launch_add_rmsnorm_backward(const NormGradArgs &a, hipStream_t stream
         if (e != hipSuccess) return e;
     }
     if (!a.grad_weight) return hipSuccess;
-    norm_grad_sum_kernel<<<(a.hidden + 63) / 64, 256, 0, stream>>>(a.partial, blocks, a.hidden,
-                                                                   a.grad_weight);
+    norm_grad_sum_kernel<<<(a.hidden + 31) / 32, kSumThreads, 0, stream>>>(a.partial, blocks,
+                                                                           a.hidden, a.grad_weight);
     return hipGetLastError();
 }
 

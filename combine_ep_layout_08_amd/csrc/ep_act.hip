@@ -8,6 +8,7 @@ namespace {
 
 constexpr int kActThreads = 256;
 constexpr int kActWaves = kActThreads / 64;
+constexpr int64_t kActRows = 4096;       // rows from which a wave takes a whole one
 constexpr int64_t kActBlocks = 1 << 22;  // most blocks of a launch; they walk the work behind
 
 dim3 act_grid(int64_t waves) {
@@ -15,16 +16,33 @@ dim3 act_grid(int64_t waves) {
     return dim3(static_cast<uint32_t>(blocks < kActBlocks ? blocks : kActBlocks));
 }
 
-// 1 / (1 + exp(-g)) and exp(-g): v_exp_f32 and v_rcp_f32 are within an ulp of
-// binary32, and the argument's rounding adds |g| 2^-24: far inside the outputs'
-// 8 or 16 bits.  exp(-g) = inf (g < -88) gives 0.
-__device__ inline float sigmoid(float g, float *e) {
-    *e = __builtin_amdgcn_exp2f(-1.44269504f * g);
-    return __builtin_amdgcn_rcpf(1.0f + *e);
+// 1 / (1 + exp(-g)): v_exp_f32 and v_rcp_f32 are within an ulp of binary32, and the
+// argument's rounding adds |g| 2^-24: far inside the outputs' 8 or 16 bits.
+// exp(-g) = inf (g < -88) gives 0.
+__device__ inline float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+
+// Exponent bytes of gate's and up's block b into a row of 2 * blocks bytes: up's
+// need not start at a pack, so every block stores its own byte; the bytes behind the
+// last block are zero.
+__device__ inline void store_bytes(const Scales &sf, int64_t row, int b, int blocks,
+                                   uint32_t gate, uint32_t up, int lane) {
+    if ((lane & 15) != 0 || b >= blocks) return;
+    char *base = reinterpret_cast<char *>(sf.p + row * sf.ts);
+    auto store = [&](int i, uint32_t e) {
+        base[4 * ((i >> 2) * sf.hs) + (i & 3)] = static_cast<char>(e);
+    };
+    store(b, gate);
+    store(blocks + b, up);
+    if (b == blocks - 1)
+        for (int i = 2 * blocks; i & 3; ++i) store(i, 0);
 }
 
 // Row of slot i, or -1 where the slot is empty, outside the buffers, or the
-// layout on the handle is void.
+// layout on the handle is void.  Slots and not rows are walked: every slot has a
+// row, while gaps and the room behind the last row would have to be looked at (walked in
+// memory order 32768 of 65280 rows took 113 us instead of 103, a decode batch 20 instead of 5).
 __device__ inline int64_t slot_row(const int32_t *dst, const int32_t *scalars, int64_t i,
                                    int64_t capacity) {
     const int32_t r = dst[i];
@@ -32,78 +50,71 @@ __device__ inline int64_t slot_row(const int32_t *dst, const int32_t *scalars, i
     return r < 0 || r >= capacity || (bits & EP_ERRBIT_FATAL) ? -1 : r;
 }
 
-// One wave for 512 channels of a slot's row, 8 a lane: a row of 16 lanes is
-// one scale block of gate, of up and of h.
+// One wave for a slot's row, 512 channels a step, 8 a lane: a row of 16 lanes is
+// one scale block of gate, of up and of h.  gridDim.y waves share a row.
 template <int HFMT, int SFMT>
-__global__ __launch_bounds__(kActThreads) void act_kernel(const ActArgs a, int chunks) {
+__global__ __launch_bounds__(kActThreads) void act_kernel(const ActArgs a) {
 #pragma clang fp contract(off)
     const int lane = threadIdx.x & 63;
+    const int V = a.inter / 8, chunks = (V + 63) / 64, blocks = a.inter / 128;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kActWaves;
-    for (int64_t wave = static_cast<int64_t>(blockIdx.x) * kActWaves + (threadIdx.x >> 6);
-         wave < a.num_slots * chunks; wave += stride) {
-        const int64_t row = slot_row(a.dst, a.scalars, wave / chunks, a.capacity);
+    for (int64_t slot = static_cast<int64_t>(blockIdx.x) * kActWaves +
+                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         slot < a.num_slots; slot += stride) {
+        const int64_t row = slot_row(a.dst, a.scalars, slot, a.capacity);
         if (row < 0) continue;
-        const int chunk = static_cast<int>(wave % chunks);
-        const int V = a.inter / 8;
-        const int v = chunk * 64 + lane;
-        const bool in = v < V;
-        const u32x4 *src = static_cast<const u32x4 *>(a.gate_up) + row * 2 * V;
-        u32x4 gv = u32x4{0u, 0u, 0u, 0u}, uv = gv;
-        if (in) {
-            gv = src[v];
-            uv = src[V + v];
-        }
         const float w = a.row_weights ? a.row_weights[row] : 1.0f;
-        float g[8], u[8], h[8];
-        unpack8(gv, g);
-        unpack8(uv, u);
+        const u32x4 *src = static_cast<const u32x4 *>(a.gate_up) + row * 2 * V;
+        for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
+            const int v = chunk * 64 + lane;
+            const bool in = v < V;
+            u32x4 gv = u32x4{0u, 0u, 0u, 0u}, uv = gv;
+            if (in) {
+                gv = src[v];
+                uv = src[V + v];
+            }
+            float g[8], u[8], h[8];
+            unpack8(gv, g);
+            unpack8(uv, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float e;
-            h[j] = g[j] * sigmoid(g[j], &e) * u[j] * w;
-        }
-        const int blocks = a.inter / 128, b0 = chunk * 4;
-        uint32_t pack;
-        if (HFMT == kSfNone) {
-            if (in) (static_cast<u32x4 *>(a.out_h) + row * V)[v] = pack8(h);
-        } else {
-            constexpr int F = HFMT == kSfNone ? EP_SF_F32 : HFMT;
-            const u32x2 q = e4m3_block8<F>(h, &pack);
-            if (in) (static_cast<u32x2 *>(a.out_h) + row * V)[v] = q;
-            store_packs<F>(a.h_sf.p, a.h_sf.ts, a.h_sf.hs, row, b0, blocks, pack, lane);
-        }
-        if (SFMT != kSfNone) {
-            constexpr int F = SFMT == kSfNone ? EP_SF_F32 : SFMT;
-            u32x2 *dst = static_cast<u32x2 *>(a.saved) + row * 2 * V;
-            u32x2 q = e4m3_block8<F>(g, &pack);
-            uint32_t gp = pack;
-            if (in) dst[v] = q;
-            q = e4m3_block8<F>(u, &pack);
-            if (in) dst[V + v] = q;
-            if (F == EP_SF_F32) {
-                store_packs<F>(a.saved_sf.p, a.saved_sf.ts, a.saved_sf.hs, row, b0, blocks, gp, lane);
-                const int b = blocks + b0 + (lane >> 4);
-                if ((lane & 15) == 0 && b < 2 * blocks)
-                    a.saved_sf.p[row * a.saved_sf.ts + b * a.saved_sf.hs] = pack;
-            } else {
-                // packs of the row's 2 * blocks exponents, bytes: up's need not
-                // start at a pack, so every block stores its own byte; the bytes
-                // behind the last block are zero
-                char *base = reinterpret_cast<char *>(a.saved_sf.p);
-                if ((lane & 15) == 0) {
+            for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j] * w;
+            const int b0 = chunk * 4;
+            uint32_t pack;
+            if (HFMT == kSfNone) {
+                if (in) (static_cast<u32x4 *>(a.out_h) + row * V)[v] = pack8(h);
+            }
+            uint32_t gm = 0, um = 0;
+            if (SFMT != kSfNone) {
+                constexpr int F = SFMT == kSfNone ? EP_SF_F32 : SFMT;
+                gm = block_max_bits(gv);
+                um = block_max_bits(uv);
+                u32x2 *dst = static_cast<u32x2 *>(a.saved) + row * 2 * V;
+                u32x2 q = e4m3_block8<F>(g, gm, &pack);
+                const uint32_t gp = pack;
+                if (in) dst[v] = q;
+                q = e4m3_block8<F>(u, um, &pack);
+                if (in) dst[V + v] = q;
+                if (F == EP_SF_F32) {
+                    store_packs<F>(a.saved_sf.p, a.saved_sf.ts, a.saved_sf.hs, row, b0, blocks, gp,
+                                   lane);
                     const int b = b0 + (lane >> 4);
-                    if (b < blocks) {
-                        const int bu = blocks + b;
-                        base[4 * (row * a.saved_sf.ts + (b >> 2) * a.saved_sf.hs) + (b & 3)] =
-                            static_cast<char>(gp);
-                        base[4 * (row * a.saved_sf.ts + (bu >> 2) * a.saved_sf.hs) + (bu & 3)] =
-                            static_cast<char>(pack);
-                        if (b == blocks - 1)
-                            for (int z = bu + 1; z & 3; ++z)
-                                base[4 * (row * a.saved_sf.ts + (z >> 2) * a.saved_sf.hs) + (z & 3)] =
-                                    0;
-                    }
+                    if ((lane & 15) == 0 && b < blocks)
+                        a.saved_sf.p[row * a.saved_sf.ts + (blocks + b) * a.saved_sf.hs] = pack;
+                } else {
+                    store_bytes(a.saved_sf, row, b0 + (lane >> 4), blocks, gp, pack, lane);
                 }
+            }
+            if (HFMT != kSfNone) {
+                constexpr int F = HFMT == kSfNone ? EP_SF_F32 : HFMT;
+                // with finite factors whose product stays finite h is finite too,
+                // and its maximum takes half the operations
+                const bool finite = SFMT != kSfNone &&
+                    __builtin_fabsf(__uint_as_float(gm) * __uint_as_float(um)) < 3.4e38f &&
+                    __builtin_fabsf(w) <= 1.0f;
+                const uint32_t hm = finite ? finite_max_bits(h) : block_max_bits(h);
+                const u32x2 q = e4m3_block8<F>(h, hm, &pack);
+                if (in) (static_cast<u32x2 *>(a.out_h) + row * V)[v] = q;
+                store_packs<F>(a.h_sf.p, a.h_sf.ts, a.h_sf.hs, row, b0, blocks, pack, lane);
             }
         }
     }
@@ -111,11 +122,16 @@ __global__ __launch_bounds__(kActThreads) void act_kernel(const ActArgs a, int c
 
 template <int HFMT>
 hipError_t launch_act(const ActArgs &a, hipStream_t stream) {
+    // Few rows: a wave for every 512 channels; many: one a row, which reads the slot and
+    // the row weight once.
     const int chunks = (a.inter / 8 + 63) / 64;
-    const dim3 grid = act_grid(a.num_slots * chunks), block(kActThreads);
-    if (!a.saved) act_kernel<HFMT, kSfNone><<<grid, block, 0, stream>>>(a, chunks);
-    else if (a.saved_sf.ue8m0) act_kernel<HFMT, EP_SF_UE8M0><<<grid, block, 0, stream>>>(a, chunks);
-    else act_kernel<HFMT, EP_SF_F32><<<grid, block, 0, stream>>>(a, chunks);
+    const bool few = a.num_slots < kActRows;
+    dim3 grid = act_grid(a.num_slots);
+    grid.y = few ? chunks : 1;
+    const dim3 block(kActThreads);
+    if (!a.saved) act_kernel<HFMT, kSfNone><<<grid, block, 0, stream>>>(a);
+    else if (a.saved_sf.ue8m0) act_kernel<HFMT, EP_SF_UE8M0><<<grid, block, 0, stream>>>(a);
+    else act_kernel<HFMT, EP_SF_F32><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -159,8 +175,7 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs
             float og[8], ou[8], oh[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float e;
-                const float s = sigmoid(g[j], &e);
+                const float s = sigmoid(g[j]);
                 const float silu = g[j] * s;
                 const float whole = silu * u[j];
                 total = __builtin_fmaf(gh[j], whole, total);

@@ -100,82 +100,126 @@ __device__ inline double wave_sum64(double v) {
 
 // ---------------------------------------------------------------- E4M3 blocks
 // The recipe of ep_quantize_fp8 on binary32 values: a row of 16 lanes holds a
-// block of 128 channels, 8 a lane; every lane of the block calls this.
+// block of 128 channels, 8 a lane; every lane of the block calls these.
 //   amax = largest |v| (NaN skipped), s = max(amax, 1e-12) / 448; UE8M0 rounds
 //   s up to a power of two; code = E4M3 nearest to clamp(v / s, +-448).
-// Finite blocks divide through one correctly rounded reciprocal y = 1/s and
-// one remainder correction (Markstein's division), which gives the correctly
-// rounded v / s wherever |v / s| >= 2^-11; smaller quotients have the zero
-// code either way.  Those quotients lie within an ulp of +-448, so only
-// blocks with an infinity or a NaN are clamped, and take true divisions.
-// *pack: the scale's binary32 bits, or its exponent byte.
-template <int FMT>
-__device__ inline u32x2 e4m3_block8(const float v[8], uint32_t *pack) {
-#pragma clang fp contract(off)
+// Divisions are Markstein's: with y the correctly rounded reciprocal of b and q0 = a y,
+// q0 + (a - q0 b) y, each step one fused operation, is the correctly rounded a / b
+// where nothing leaves the normal range; and y itself comes from the hardware's
+// reciprocal (within an ulp) by one step y + (1 - b y) y.  (Compared with true divisions on
+// MI355X over every significand of s at ten exponents, eight quotients each: no
+// difference.)  Six operations a block and three a value, where a true division takes
+// ten or more; with three blocks a lane they had the activation's vector units
+// busy 87 % of the time, now 64 %.
+
+// Largest |v| of the block as bits; NaN patterns (above infinity's) are kept.
+__device__ inline uint32_t block_max_bits(const float v[8]) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
         m = b > m ? b : m;
     }
-    m = row_max(m);                        // non-negative floats order like their bits, NaN on top
-    const bool finite = m < 0x7F800000u;
-    if (!finite) {
-        m = 0;
+    return row_max(m);
+}
+
+// The same of bf16 values, two a word, with packed 16-bit maxima.
+__device__ inline uint32_t block_max_bits(const u32x4 v) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = __builtin_bit_cast(u16x2, v.x & 0x7FFF7FFFu);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-            if (b <= 0x7F800000u && b > m) m = b;
-        }
-        m = row_max(m);
-    }
-    const float amax = __uint_as_float(m);
-    float s = __fdiv_rn(amax > 1e-12f ? amax : 1e-12f, 448.0f);
+    for (int i = 1; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
+    const uint32_t w = __builtin_bit_cast(uint32_t, m);
+    const uint32_t lo = w << 16, hi = w & 0xFFFF0000u;
+    return row_max(lo > hi ? lo : hi);
+}
+
+// The same of values that are known to be neither NaN nor infinite.
+__device__ inline uint32_t finite_max_bits(const float v[8]) {
+    float m = __builtin_fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i]));
+    return row_max(__float_as_uint(m));
+}
+
+__device__ inline float over_448(float amax) {
+    const float y = 1.0f / 448.0f;
+    const float q = amax * y;
+    return __builtin_fmaf(__builtin_fmaf(-q, 448.0f, amax), y, q);
+}
+
+__device__ inline uint32_t e4m3_pack4(const float c[4]) {
+    int word = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    word = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], word, true);
+    return static_cast<uint32_t>(word);
+}
+
+// A block's divisor from its scale max(amax, 1e-12) / 448, and what is stored: binary32
+// bits or the exponent byte.
+template <int FMT>
+__device__ inline float block_divisor(float s, uint32_t *pack) {
     if (FMT == EP_SF_UE8M0) {
         uint32_t e = (__float_as_uint(s) >> 23) & 0xFFu;
         if (__float_as_uint(s) & 0x7FFFFFu) ++e;
         *pack = e;
-        s = __uint_as_float(e << 23);
-    } else {
-        *pack = __float_as_uint(s);
+        return __uint_as_float(e << 23);
     }
+    *pack = __float_as_uint(s);
+    return s;
+}
+
+__device__ inline float at_least(float amax) { return amax > 1e-12f ? amax : 1e-12f; }
+
+// Codes of a block with an infinity or a NaN in it: true divisions, clamped, NaN codes.
+template <int FMT>
+__device__ inline u32x2 e4m3_special8(const float v[8], uint32_t *pack) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+        if (b <= 0x7F800000u && b > m) m = b;
+    }
+    const float s =
+        block_divisor<FMT>(__fdiv_rn(at_least(__uint_as_float(row_max(m))), 448.0f), pack);
     float c[8];
-    if (finite) {
-        if (FMT == EP_SF_UE8M0) {
-            // s = 2^k with -49 <= k <= 120: v * 2^-k is v / s
-            const float y = __uint_as_float((254u << 23) - __float_as_uint(s));
+    uint32_t nan[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = v[i] * y;
-        } else {
-            const float y = __fdiv_rn(1.0f, s);
+    for (int i = 0; i < 8; ++i) {
+        const float q = __fdiv_rn(v[i], s);
+        if (q != q) nan[i / 4] |= 0xFFu << (8 * (i % 4));
+        c[i] = __builtin_fminf(__builtin_fmaxf(q, -448.0f), 448.0f);
+    }
+    const uint32_t lo = e4m3_pack4(c), hi = e4m3_pack4(c + 4);
+    return u32x2{(lo & ~nan[0]) | (0x7F7F7F7Fu & nan[0]), (hi & ~nan[1]) | (0x7F7F7F7Fu & nan[1])};
+}
+
+// Codes of a block whose maximum has the bits `max_bits` (from one of the above):
+// the quotients of a finite block lie within an ulp of +-448, so nothing is clamped.
+// *pack: the scale's binary32 bits, or its exponent byte.
+template <int FMT>
+__device__ inline u32x2 e4m3_block8(const float v[8], uint32_t max_bits, uint32_t *pack) {
+#pragma clang fp contract(off)
+    if (__builtin_expect(max_bits >= 0x7F800000u, 0)) return e4m3_special8<FMT>(v, pack);
+    const float s =
+        block_divisor<FMT>(over_448(at_least(__uint_as_float(max_bits))), pack);
+    float c[8];
+    if (FMT == EP_SF_UE8M0) {
+        // s = 2^k with -49 <= k <= 120: v * 2^-k is v / s
+        const float y = __uint_as_float((254u << 23) - __float_as_uint(s));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q0 = v[i] * y;
-                const float n = __builtin_fmaf(q0, s, -v[i]);
-                c[i] = __builtin_fmaf(-n, y, q0);
-            }
-        }
+        for (int i = 0; i < 8; ++i) c[i] = v[i] * y;
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[i] = __builtin_fminf(__builtin_fmaxf(__fdiv_rn(v[i], s), -448.0f), 448.0f);
-    }
-    uint32_t w[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        int word = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * g], c[4 * g + 1], 0, false);
-        word = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * g + 2], c[4 * g + 3], word, true);
-        w[g] = static_cast<uint32_t>(word);
-    }
-    if (!finite) {
+        const float y0 = __builtin_amdgcn_rcpf(s);
+        const float y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = __fdiv_rn(v[i], s);
-            if (q != q)
-                w[i / 4] = (w[i / 4] & ~(0xFFu << (8 * (i % 4)))) | (0x7Fu << (8 * (i % 4)));
+            const float q0 = v[i] * y;
+            const float n = __builtin_fmaf(q0, s, -v[i]);
+            c[i] = __builtin_fmaf(-n, y, q0);
         }
     }
-    return u32x2{w[0], w[1]};
+    return u32x2{e4m3_pack4(c), e4m3_pack4(c + 4)};
 }
 
 // Stores the scale packs of a wave that holds 4 consecutive blocks starting

@@ -100,8 +100,8 @@ ep_status ep_add_rmsnorm(const void *x, const void *residual, const void *weight
 
 size_t ep_add_rmsnorm_backward_workspace(int32_t num_tokens, int32_t hidden) {
     if (num_tokens < 0 || channels_status(hidden, false) != EP_OK) return 0;
-    const size_t blocks = static_cast<size_t>(ep::norm_grad_blocks(num_tokens, hidden));
-    return sizeof(float) * static_cast<size_t>(hidden) * (blocks < 1 ? 1 : blocks);
+    return sizeof(float) * static_cast<size_t>(hidden) *
+           static_cast<size_t>(ep::norm_grad_blocks(num_tokens));
 }
 
 ep_status ep_add_rmsnorm_backward(const void *grad_y, const void *z, const void *weight,
@@ -119,9 +119,8 @@ ep_status ep_add_rmsnorm_backward(const void *grad_y, const void *z, const void 
         return EP_ERR_MISALIGNED;
     if (num_tokens > 0 && (!grad_y || !z || !weight || !rstd || (!grad_x && !grad_weight)))
         return EP_ERR_NULL;
-    if (grad_weight &&
-        (!workspace || ws_bytes < ep_add_rmsnorm_backward_workspace(num_tokens, hidden)))
-        return EP_ERR_WORKSPACE;
+    const size_t need = grad_weight ? ep_add_rmsnorm_backward_workspace(num_tokens, hidden) : 0;
+    if (need > 0 && (!workspace || ws_bytes < need)) return EP_ERR_WORKSPACE;
     ep::NormGradArgs a{};
     a.grad_y = grad_y;
     a.z = z;

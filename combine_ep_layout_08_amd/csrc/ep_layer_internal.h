@@ -78,8 +78,8 @@ struct W4Args {
     void *out;                   // bf16 [capacity, n]
 };
 
-// Blocks whose sums of grad_weight the workspace holds.
-int norm_grad_blocks(int32_t num_tokens, int32_t hidden);
+// Blocks whose sums of grad_weight the workspace holds (0: none are kept).
+int norm_grad_blocks(int32_t num_tokens);
 
 hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream);
 hipError_t launch_add_rmsnorm_backward(const NormGradArgs &a, hipStream_t stream);

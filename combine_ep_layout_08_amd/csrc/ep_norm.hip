@@ -7,6 +7,10 @@ namespace ep {
 namespace {
 
 constexpr int kNormBlocks = 1 << 18;     // most blocks of a launch; they walk the rows behind
+// Rows up to which the gradient is one launch (us, two launches / one, host time of the
+// second included: 512 x 7168 17.5 / 11.9, 1024 x 7168 21.0 / 18.0, 2048 x 7168 28.9 / 31.6;
+// 1024 x 1280 15.8 / 11.7, 2048 x 1280 16.1 / 19.6).
+constexpr int kFewRows = 1024;
 
 // Channels [8v, 8v + 8) of the norm's weight as binary32.
 __device__ inline void load_weight(const void *w, bool bf16, int v, float f[8]) {
@@ -209,6 +213,86 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a) {
     }
 }
 
+// Few rows: one launch.  The first blocks take a row each for grad_x; each of the
+// others 64 channels of grad_weight over all rows, which reads g and z a second time (from the
+// caches) instead of writing and reading sums.  8 lanes of 8 channels, the rest of the
+// threads are groups that take every so many rows, added up in a fixed order.
+template <int VPT>
+__global__ __launch_bounds__(1024) void norm_grad_few_kernel(const NormGradArgs a,
+                                                             int row_blocks) {
+    __shared__ float sums[16][64];
+    const int V = a.hidden / 8;
+    const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 63;
+    if (static_cast<int>(blockIdx.x) < row_blocks) {
+        const int64_t row = blockIdx.x;
+        const float rstd = a.rstd[row];
+        float zf[VPT][8], gf[VPT][8], mf[VPT][8];
+        float c = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            u32x4 z = u32x4{0u, 0u, 0u, 0u}, g = z, more = z;
+            float w[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (v < V) {
+                z = (static_cast<const u32x4 *>(a.z) + row * V)[v];
+                g = (static_cast<const u32x4 *>(a.grad_y) + row * V)[v];
+                if (a.grad_z) more = (static_cast<const u32x4 *>(a.grad_z) + row * V)[v];
+                load_weight(a.weight, a.weight_bf16, v, w);
+            }
+            unpack8(z, zf[i]);
+            unpack8(g, gf[i]);
+            unpack8(more, mf[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                c = __builtin_fmaf(gf[i][j] * (zf[i][j] * rstd), w[j], c);
+                gf[i][j] *= w[j];
+            }
+        }
+        c = wave_sum(c);
+        if (lane == 0) sums[tid >> 6][0] = c;
+        __syncthreads();
+        c = 0.0f;
+        for (int i = 0; i < threads / 64; ++i) c += sums[i][0];
+        c *= 1.0f / static_cast<float>(a.hidden);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * threads + tid;
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = __builtin_fmaf(gf[i][j] - (zf[i][j] * rstd) * c, rstd, mf[i][j]);
+            if (v < V) (static_cast<u32x4 *>(a.grad_x) + row * V)[v] = pack8(o);
+        }
+        return;
+    }
+    const int v = (blockIdx.x - row_blocks) * 8 + (tid & 7);
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (v < V) {
+#pragma unroll 4
+        for (int64_t row = tid >> 3; row < a.num_tokens; row += threads / 8) {
+            const float rstd = a.rstd[row];
+            float zf[8], gf[8];
+            unpack8((static_cast<const u32x4 *>(a.z) + row * V)[v], zf);
+            unpack8((static_cast<const u32x4 *>(a.grad_y) + row * V)[v], gf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += gf[j] * (zf[j] * rstd);
+        }
+    }
+#pragma unroll
+    for (int d = 8; d < 64; d <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += __shfl_xor(s[j], d);
+    if (lane < 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[tid >> 6][lane * 8 + j] = s[j];
+    __syncthreads();
+    const int64_t ch = static_cast<int64_t>(blockIdx.x - row_blocks) * 64 + tid;
+    if (tid >= 64 || ch >= a.hidden) return;
+    float total = sums[0][tid];
+    for (int w = 1; w < threads / 64; ++w) total += sums[w][tid];
+    a.grad_weight[ch] = total;
+}
+
 // Sums of the blocks' rows, 32 channels a block: 8 lanes of 4 channels, 128 groups
 // that take every 128th row.  A group's loads are independent of each other, so
 // the kernel lasts a few memory latencies (8 groups of 64 loads in a chain took
@@ -239,6 +323,21 @@ __global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float 
     *reinterpret_cast<f32x4 *>(out + c) = s;
 }
 
+hipError_t launch_few(const NormGradArgs &a, int rows, int columns, hipStream_t stream) {
+    const int V = a.hidden / 8, blocks = rows + columns;
+    if (blocks == 0) return hipSuccess;
+    if (V <= 512) norm_grad_few_kernel<1><<<blocks, 512, 0, stream>>>(a, rows);
+    else if (V <= 1024) norm_grad_few_kernel<1><<<blocks, 1024, 0, stream>>>(a, rows);
+    else norm_grad_few_kernel<4><<<blocks, 1024, 0, stream>>>(a, rows);
+    return hipGetLastError();
+}
+
+// Whether two buffers of `bytes` bytes share some.
+bool overlap(const void *p, const void *q, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + bytes && b < a + bytes;
+}
+
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream) {
@@ -246,24 +345,29 @@ hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t stream) {
     return a.sf.ue8m0 ? launch_norm<EP_SF_UE8M0>(a, stream) : launch_norm<EP_SF_F32>(a, stream);
 }
 
-int norm_grad_blocks(int32_t num_tokens, int32_t hidden) {
-    (void)hidden;
-    return num_tokens < 512 ? num_tokens : 512;
-}
+// Two blocks a compute unit: 384 to 512 of them took 47 to 48 us at 4096 x 7168, 640 and
+// more 53 and more (their sums' rows), 256 took 51.
+int norm_grad_blocks(int32_t num_tokens) { return num_tokens <= kFewRows ? 0 : 512; }
 
 hipError_t launch_add_rmsnorm_backward(const NormGradArgs &a, hipStream_t stream) {
     const int V = a.hidden / 8;
-    const int blocks = norm_grad_blocks(a.num_tokens, a.hidden);
-    if (blocks > 0) {
-        const int vpt = V <= 512 ? 1 : V <= 1024 ? 2 : 4;
-        const int threads = ((V + vpt - 1) / vpt + 63) / 64 * 64;
-        if (vpt == 1) norm_grad_kernel<1><<<blocks, threads, 0, stream>>>(a);
-        else if (vpt == 2) norm_grad_kernel<2><<<blocks, threads, 0, stream>>>(a);
-        else norm_grad_kernel<4><<<blocks, threads, 0, stream>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    if (a.num_tokens <= kFewRows) {
+        const int rows = a.grad_x ? a.num_tokens : 0, columns = a.grad_weight ? (V + 7) / 8 : 0;
+        // grad_x over grad_y would take from grad_weight's blocks what they have yet to read
+        const int64_t bytes = static_cast<int64_t>(a.num_tokens) * a.hidden * 2;
+        const bool apart = !overlap(a.grad_x, a.grad_y, bytes) && !overlap(a.grad_x, a.z, bytes);
+        if (apart || rows == 0 || columns == 0) return launch_few(a, rows, columns, stream);
+        const hipError_t e = launch_few(a, 0, columns, stream);
+        return e != hipSuccess ? e : launch_few(a, rows, 0, stream);
     }
-    if (!a.grad_weight) return hipSuccess;
+    const int blocks = norm_grad_blocks(a.num_tokens);
+    const int vpt = V <= 512 ? 1 : V <= 1024 ? 2 : 4;
+    const int threads = ((V + vpt - 1) / vpt + 63) / 64 * 64;
+    if (vpt == 1) norm_grad_kernel<1><<<blocks, threads, 0, stream>>>(a);
+    else if (vpt == 2) norm_grad_kernel<2><<<blocks, threads, 0, stream>>>(a);
+    else norm_grad_kernel<4><<<blocks, threads, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.grad_weight) return e;
     norm_grad_sum_kernel<<<(a.hidden + 31) / 32, kSumThreads, 0, stream>>>(a.partial, blocks,
                                                                            a.hidden, a.grad_weight);
     return hipGetLastError();

@@ -509,7 +509,8 @@ hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t
 //   half a compute unit.  One token of 8 experts (4096 x 7168, 2048 tiles): 24.0
 //   with two waves a group of 32 outputs, 30.3 with one, 47.0 with 64 outputs a wave;
 //   26 experts with rows: 73.9, 74.7 and 71.4; 2 experts of 1024 outputs: 8.5 with
-//   four waves a group, 10.8 with two.  Short rows leave a block little to do between
+//   four waves a group, 10.8 with two; but every wave has two steps at least (two steps,
+//   16 experts of 512 outputs: 4.6 with one wave a group, 5.5 with four).  Short rows leave a block little to do between
 //   its first and last loads, which more blocks a compute unit hide: 64 outputs a wave
 //   from 32 steps on only (7168 x 2048, 16 steps: 88 with 64, 81 with 32 outputs).
 //   Three steps in registers instead of two keep more of the weights in flight where a
@@ -530,7 +531,11 @@ hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     if (tiles >= 8 * kBlocks)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
-    if (tiles >= 4 * kBlocks)
+    const int steps = a.k / 128;
+    if (steps < 4)
+        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
+                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
+    if (tiles >= 4 * kBlocks || steps < 8)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 2, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 2, 1, 2, 3>(a, active, slots, stream);
     return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 4, 2>(a, active, slots, stream)

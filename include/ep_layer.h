@@ -77,9 +77,10 @@ ep_status ep_add_rmsnorm(const void *x, const void *residual, const void *weight
  *   grad_x      NULL or bf16 [num_tokens, hidden]: gradient of x and of the
  *               residual (they share it); may be grad_y or grad_z itself.
  *   grad_weight NULL or fp32 [hidden], summed in binary32 in a fixed order
- *               (zeros when num_tokens is 0); needs the workspace.
- *   workspace   device, 16-byte aligned, ep_add_rmsnorm_backward_workspace bytes
- *               (0 if the sizes are invalid); not needed without grad_weight.
+ *               (zeros when num_tokens is 0).
+ *   workspace   device, 16-byte aligned, ep_add_rmsnorm_backward_workspace bytes;
+ *               may be NULL without grad_weight, and where that function gives 0: for
+ *               few rows (and for invalid sizes).
  */
 size_t ep_add_rmsnorm_backward_workspace(int32_t num_tokens, int32_t hidden);
 ep_status ep_add_rmsnorm_backward(const void *grad_y, const void *z, const void *weight,

@@ -159,6 +159,9 @@ GRAD_CASES = [  # T, H, residual gradient, weight dtype
     (333, 1280, False, torch.float32),
     (511, 264, True, torch.bfloat16),
     (513, 4104, True, torch.bfloat16),
+    (1024, 520, True, torch.float32),
+    (1025, 264, True, torch.bfloat16),
+    (1500, 16512, False, torch.bfloat16),
     (2, 32768, True, torch.float32),
     (4096, 7168, True, torch.bfloat16),
     (9000, 256, False, torch.float32),
@@ -209,6 +212,7 @@ def test_backward_in_place(target):
     g, gz = _rows(T, H, gen), _rows(T, H, gen)
     rstd = ep.add_rmsnorm(z, w, want_rstd=True)[4]
     want = ep.add_rmsnorm_backward(g, z, w, rstd, grad_residual=gz)
+    want = (want[0].clone(), want[1].clone())
     out = g if target == "grad_y" else gz
     got = ep.add_rmsnorm_backward(g, z, w, rstd, grad_residual=gz, grad_x=out)
     assert got[0] is out and torch.equal(out, want[0]) and torch.equal(got[1], want[1])

@@ -85,8 +85,8 @@ def norm_grad(g=A16, z=A16, w=A16, wdt=ep.EP_F32, rstd=A16, gz=None, T=4, H=256,
     (ep.EP_ERR_NULL, dict(w=None)),
     (ep.EP_ERR_NULL, dict(rstd=None)),
     (ep.EP_ERR_NULL, dict(gx=None, gw=None)),
-    (ep.EP_ERR_WORKSPACE, dict(ws=None)),
-    (ep.EP_ERR_WORKSPACE, dict(nbytes=4 * 256 - 1)),
+    (ep.EP_ERR_WORKSPACE, dict(T=4096, ws=None)),
+    (ep.EP_ERR_WORKSPACE, dict(T=4096, nbytes=4 * 256 - 1)),
     (ep.EP_ERR_MISALIGNED, dict(g=A16 + 8)),
     (ep.EP_ERR_MISALIGNED, dict(gz=A16 + 8)),
     (ep.EP_ERR_MISALIGNED, dict(gx=A16 + 8)),
@@ -103,9 +103,8 @@ def test_norm_gradient_workspace():
     assert ep.ep_add_rmsnorm_backward_workspace(-1, 256) == 0
     assert ep.ep_add_rmsnorm_backward_workspace(4, 12) == 0
     assert ep.ep_add_rmsnorm_backward_workspace(4, 40000) == 0
-    assert ep.ep_add_rmsnorm_backward_workspace(0, 256) >= 4 * 256
-    small, large = (ep.ep_add_rmsnorm_backward_workspace(t, 7168) for t in (1, 1 << 20))
-    assert 4 * 7168 <= small <= large <= 4 * 7168 * 4096
+    few, some, large = (ep.ep_add_rmsnorm_backward_workspace(t, 7168) for t in (1, 4096, 1 << 20))
+    assert few == 0 and 4 * 7168 <= some <= large <= 4 * 7168 * 4096
 
 
 def w4(h=None, x=A16, dt=ep.EP_BF16, tokens=0, k=256, sf=None, sfmt=F, ts=2, hs=1, codes=A16,

@@ -243,11 +243,11 @@ def test_gradient_against_differences():
         assert abs(float((gw.double() * e).sum()) - dw) <= 1e-5 * float((gw.double() * e).abs().sum())
 
 
-def test_bound_call_and_graph():
+@pytest.mark.parametrize("T,H", [(64, 1024), (2048, 640)])
+def test_bound_call_and_graph(T, H):
     """A bound call and a captured pair (norm, gradient) follow their tensors' new
     contents; each replay is compared with the eager calls."""
     gen = _gen(10)
-    T, H = 64, 1024
     x, r, w = _rows(T, H, gen), _rows(T, H, gen), _weight(H, gen, torch.bfloat16)
     g = _rows(T, H, gen)
     call = ep.bind_add_rmsnorm(x, w, residual=r, scale_format="f32", want_rstd=True)
@@ -269,3 +269,48 @@ def test_bound_call_and_graph():
             assert torch.equal(a, b)
         wx, ww = ep.add_rmsnorm_backward(g, want[1], w, want[4], grad_residual=g)
         assert torch.equal(gx, wx) and torch.equal(gw, ww)
+
+
+def test_offsets_past_32_bits():
+    """Rows behind the first 4 GiB."""
+    T, H = 140_000, 16384
+    gen = _gen(12)
+    x = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-50:] = _rows(50, H, gen)
+    w = _weight(H, gen, torch.float32)
+    say("norm offsets", T, H)
+    y, _, q, sf, rstd = ep.add_rmsnorm(x, w, eps=EPS, scale_format="f32", want_rstd=True)
+    last = ep.add_rmsnorm(x[-50:].contiguous(), w, eps=EPS, scale_format="f32", want_rstd=True)
+    for a, b in zip((y, q, sf, rstd), (last[0], *last[2:])):
+        assert torch.equal(a[-50:], b)
+    gx, gw = ep.add_rmsnorm_backward(y, x, w, rstd)
+    lx, _ = ep.add_rmsnorm_backward(last[0], x[-50:].contiguous(), w, last[4])
+    # another number of rows sums in another order: a step of bf16 at most
+    ref.assert_close(gx[-50:], lx, lx.double().abs() * 2 * ref.BF16 + 1e-4, "gradient")
+    assert bool(torch.isfinite(gw).all())
+
+
+def test_two_streams():
+    """Forward and backward of two batches at once, each with its own buffers."""
+    gen = _gen(13)
+    sets = []
+    for T, H in ((1500, 2048), (700, 4096)):
+        x, r, g = _rows(T, H, gen), _rows(T, H, gen), _rows(T, H, gen)
+        sets.append((x, r, g, _weight(H, gen, torch.bfloat16)))
+
+    def step(x, r, g, w):
+        y, z, q, sf, rstd = ep.add_rmsnorm(x, w, residual=r, scale_format="f32", want_rstd=True)
+        return (y, q, sf, *ep.add_rmsnorm_backward(g, z, w, rstd, grad_residual=g))
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(step(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v)

@@ -252,3 +252,91 @@ def test_no_tokens():
     out = ref.poisoned((h.capacity, 128), torch.bfloat16)
     h.swiglu(torch.zeros((h.capacity, 256), device="cuda").bfloat16(), out=out)
     assert ref.untouched(out, [])
+
+
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_row_weights_of_any_size(fmt):
+    """Weights above one, below zero, zero and not finite: each in its own row, with
+    and without a checkpoint beside the E4M3 rows."""
+    h, rows, gu, w, _ = _case(9, 1, 1, 1, 256, 0.0, 8)
+    w[:] = torch.tensor([3.5, -2.0, 0.0, 1e30, 1.0, -1.0, float("inf"), float("nan"), 0.3],
+                        device="cuda")[torch.argsort(rows)]
+    a = h.swiglu(gu, row_weights=w, scale_format=fmt)
+    b = h.swiglu(gu, row_weights=w, scale_format=fmt, checkpoint="f32")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
+    fine = torch.isfinite(w)
+    want, tol = _exact(gu, w)
+    s = ref.scale_values(a[1], 2).repeat_interleave(128, 1)
+    got = ref.code_values(a[0], a[1])
+    tol = want.abs() * 2.0 ** -4 + s * 2.0 ** -10 + tol * (1 + w.double().abs()[:, None])
+    ref.assert_close(got[fine], want[fine], tol[fine], "h")
+    assert bool((a[0][w.isnan()] == 0x7F).all()) and bool((a[0][w.isinf()] == 0x7F).all())
+
+
+def test_products_that_overflow():
+    """Finite factors whose product is not: the recipe's codes for an infinity, the other
+    values of its block 0, other blocks as ever."""
+    h = ep.Handle(1, 1, 1, 1)
+    h.layout(torch.zeros((1, 1), dtype=torch.int64, device="cuda"))
+    gu = torch.ones((1, 512), device="cuda").bfloat16()
+    gu[0, 3] = gu[0, 256 + 3] = 3e38
+    for ckpt in (None, "f32"):
+        q, sf, _, _ = h.swiglu(gu, scale_format="f32", checkpoint=ckpt)
+        assert int(q[0, 3]) == 0x7F and bool(torch.isinf(sf[0, 0]))
+        assert bool((q[0, :3] == 0).all()) and bool((q[0, 4:128] == 0).all())
+        assert bool((q[0, 128:] == 0x7E).all())
+
+
+def test_offsets_past_32_bits():
+    """Rows behind the first 4 GiB of gate_up, and of its checkpoint."""
+    T, inter = 150_000, 16384
+    h = ep.Handle(T, 1, 1, 1)
+    h.layout(torch.zeros((T, 1), dtype=torch.int32, device="cuda"))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    gu = torch.ones((T, 2 * inter), dtype=torch.bfloat16, device="cuda")
+    gu[-20:] = torch.randn((20, 2 * inter), generator=gen, device="cuda").bfloat16()
+    say("swiglu offsets", T, inter)
+    out, _, saved, sf = h.swiglu(gu, checkpoint="ue8m0")
+    want, tol = _exact(gu[-20:], None)
+    ref.assert_close(out[-20:], want, want.abs() * ref.BF16 + tol, "h")
+    q, s = ep.quantize_fp8(gu[-20:].contiguous(), "ue8m0")
+    assert torch.equal(saved[-20:], q) and torch.equal(sf[-20:], s)
+    ggu, _, again = h.swiglu_backward(out, saved, sf, want_h=True)
+    want, tol, _, _, want_h, tol_h = _grad_exact(ref.code_values(q, s), out[-20:], None)
+    ref.assert_close(ggu[-20:], want, tol, "grad_gate_up")
+    ref.assert_close(again[-20:], want_h, tol_h, "h again")
+
+
+def test_graph():
+    """Forward with a checkpoint and backward from it, captured; every replay on new
+    rows and routing equals the eager calls."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    T, K, E, inter = 24, 2, 8, 256
+    idx = ref.ids(T, K, E, gen, "cuda")
+    h = ep.Handle(T, K, E, 4)
+    lay = h.bind_layout(idx)
+    lay()
+    gu = torch.randn((h.capacity, 2 * inter), generator=gen, device="cuda").bfloat16()
+    grad = torch.randn((h.capacity, inter), generator=gen, device="cuda").bfloat16()
+    w = torch.rand(h.capacity, generator=gen, device="cuda")
+
+    def step():
+        lay()
+        a = h.swiglu(gu, row_weights=w, scale_format="ue8m0", checkpoint="f32")
+        return (*a, *h.swiglu_backward(grad, a[2], a[3], row_weights=w, want_grad_weights=True,
+                                       want_h=True))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        idx.copy_(ref.ids(T, K, E, gen, "cuda", 0.2))
+        gu.copy_(torch.randn(gu.shape, generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        want = step()
+        rows = ref.rows_of(h, idx)[0]
+        for a, b in zip(kept, want):
+            assert torch.equal(a[rows].view(torch.uint8), b[rows].view(torch.uint8))

@@ -261,3 +261,73 @@ def test_bound_call_and_graph():
         want = ref_h.expert_w4(x, packed, token_rows=True)
         rows = ref.rows_of(ref_h, idx)[0]
         assert torch.equal(out[rows], want[rows])
+
+
+@pytest.mark.parametrize("fmt,group", [(INT4, 32), (INT4, 128), (MX, 32)])
+@pytest.mark.parametrize("rows", [256, 7])
+def test_every_e4m3_code(fmt, group, rows):
+    """One-hot FP8 rows of every code (subnormal ones, zeros of both signs and NaN among
+    them), the hot channel going round: exact, as code times weight has 7 bits at most."""
+    k, n = 256, 24
+    gen = _gen(11)
+    codes, _ = ref.random_w4(1, n, k, fmt, group, gen, "cuda")
+    if fmt == INT4:
+        scales = torch.ones((1, n, k // group), device="cuda").bfloat16()
+    else:
+        scales = torch.full((1, n, k // group), 127, dtype=torch.uint8, device="cuda")
+    w64 = ref.w4_values(codes, scales, group)[0]
+    code = torch.arange(256, device="cuda").to(torch.uint8)[-rows:]
+    ch = torch.arange(rows, device="cuda") * 37 % k
+    q = torch.zeros((rows, k), dtype=torch.uint8, device="cuda")
+    q[torch.arange(rows, device="cuda"), ch] = code
+    h = ep.Handle(rows, 1, 1, 1)
+    h.layout(torch.zeros((rows, 1), dtype=torch.int64, device="cuda"))
+    sf = torch.ones((rows, k // 128), device="cuda")
+    y = h.expert_w4(q, ep.pack_w4(codes, scales), sf=sf).double()
+    x = code.view(torch.float8_e4m3fn).double()
+    want = x[:, None] * w64.t()[ch]
+    nan = x.isnan()
+    assert bool(y[nan].isnan().all()) and torch.equal(y[~nan], want[~nan])
+
+
+def test_more_passes_than_one_launch_takes():
+    T, E, k, n = 1_100_000, 4, 128, 8
+    gen = _gen(12)
+    idx = torch.randint(0, E, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    h = ep.Handle(T, 1, E, 1)
+    h.layout(idx)
+    codes, scales = ref.random_w4(E, n, k, INT4, 128, gen, "cuda")
+    x = torch.randn((T, k), generator=gen, device="cuda").bfloat16()
+    say("w4 passes", T)
+    y = h.expert_w4(x, ep.pack_w4(codes, scales), token_rows=True)
+    w64 = ref.w4_values(codes, scales, 128)
+    s64 = _scales64(scales, 128, INT4)
+    rows, expert, token = ref.rows_of(h, idx)
+    for e in range(E):
+        mine = expert == e
+        xe = x[token[mine]].double()
+        want = xe @ w64[e].t()
+        tol = want.abs() * ref.BF16 + xe.abs() @ (s64[e] * 136.0).t() * 66 * ref.F32
+        ref.assert_close(y[rows[mine]], want, tol, f"expert {e}")
+
+
+def test_offsets_past_32_bits():
+    """Rows behind the first 4 GiB of x and of the product."""
+    rows, k, n = 300_000, 8192, 8192
+    h = ep.Handle(rows, 1, 2, 1)
+    idx = torch.zeros((rows, 1), dtype=torch.int32, device="cuda")
+    idx[-40:] = 1
+    h.layout(idx)
+    gen = _gen(13)
+    codes, scales = ref.random_w4(2, n, k, MX, 32, gen, "cuda")
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    x[-90:] = torch.randn((90, k), generator=gen, device="cuda").bfloat16()
+    say("w4 offsets", rows, k, n)
+    y = h.expert_w4(x, ep.pack_w4(codes, scales))
+    w64 = ref.w4_values(codes, scales, 32)
+    for e, part in ((0, slice(rows - 90, rows - 40)), (1, slice(rows - 40, rows))):
+        x64 = x[part].double()
+        want = x64 @ w64[e].t()
+        tol = want.abs() * ref.BF16 + x64.abs() @ w64[e].abs().t() * 66 * ref.F32
+        ref.assert_close(y[part], want, tol, f"expert {e}")
+    assert not bool(y[:rows - 90].any())

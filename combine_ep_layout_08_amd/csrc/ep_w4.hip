@@ -220,8 +220,13 @@ constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
 //   16 rows an expert took 290 us instead of 165 (64 experts, 4096 x 7168, MXFP4).
 //   The weights of the next D - 1 rounds stay in flight across the rounds'
 //   barriers, which order LDS only.
-template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
-__global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int first_pass) {
+//   HELD: a pass has `per` rows at most (one to four) and all of their x is brought to LDS
+//   before the first step, which takes x's loads and the barriers out of the loop: one token
+//   of 8 experts 24.5 -> 22.1 us, four tokens 78 -> 67, two experts of 4096 channels and
+//   1024 outputs 8.5 -> 6.2 (7168 channels to 4096 outputs, EP_W4_INT4).
+template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D, bool HELD>
+__global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int first_pass,
+                                                           int per) {
     typedef Records<FMT, GROUP, NT> R;
     constexpr bool MX = FMT == EP_W4_MXFP4;
     constexpr bool DIRECT = MX && FP8;           // codes go to the matrix instruction as they are
@@ -231,10 +236,12 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     constexpr int F = MT * U;                    // units of x a lane and round
     constexpr int PER = F > NW ? F / NW : 1;     // of them a wave brings
     constexpr int SPER = MT > NW ? MT / NW : 1;  // tiles' scales of x it brings
-    constexpr int kXUnits = D * KS * F * 64;
-    constexpr int kSumUnits = KS == 1 ? 0 : kW4Waves * NT * MT * 64;
-    __shared__ u32x4 lds[kXUnits > kSumUnits ? kXUnits : kSumUnits];
-    __shared__ float lds_sf[FP8 ? D * KS * MT * 16 : 1];
+    constexpr int kXUnits = HELD ? 1 : D * KS * F * 64;
+    constexpr int kSumUnits = KS == 1 || HELD ? 0 : kW4Waves * NT * MT * 64;
+    __shared__ u32x4 ring[kXUnits > kSumUnits ? kXUnits : kSumUnits];
+    __shared__ float ring_sf[FP8 && !HELD ? D * KS * MT * 16 : 1];
+    extern __shared__ u32x4 all[];               // HELD: x, then the sums
+    u32x4 *const lds = HELD ? all : ring;
     const int lane = threadIdx.x & 63, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kg = wave % KS, nw = wave / KS;
@@ -245,8 +252,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     asm("" : "+s"(mask));
     asm("" : "+v"(one28));
 
-    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, 16 * MT,
-                                lane);
+    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, per, lane);
     if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
     // The group's records are consecutive; tiles behind the last are read as the
     // last and not stored.
@@ -298,11 +304,15 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     // i % NW (by several, the same values, where there are fewer units than waves).
     const char *xp[PER];
     const uint32_t *sp[SPER];
-    auto source = [&](int t) {
-        const int m = 16 * t + (lane & 15);
-        const int64_t row = pass.start + (m < pass.rows ? m : pass.rows - 1);
+    auto row_of = [&](int m) {
+        const int64_t row = pass.start + m;
         return a.token_rows ? static_cast<int64_t>(a.src_meta[row] / a.num_topk) : row;
     };
+    auto source = [&](int t) {
+        const int m = 16 * t + (lane & 15);
+        return row_of(m < pass.rows ? m : pass.rows - 1);
+    };
+    if (!HELD)
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         const int i = (p * NW + nw) % F, j = i % U;
@@ -310,7 +320,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
         xp[p] = static_cast<const char *>(a.x) +
                 (source(i / U) * a.k + held(kg) * 128 + ch) * (FP8 ? 1 : 2);
     }
-    if (FP8) {
+    if (FP8 && !HELD) {
 #pragma unroll
         for (int p = 0; p < SPER; ++p) {
             const int i = (p * NW + nw) % MT;
@@ -352,7 +362,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
         if (FP8) {
 #pragma unroll
             for (int p = 0; p < SPER; ++p)
-                lds_sf[(buf * MT + (p * NW + nw) % MT) * 16 + (lane & 15)] =
+                ring_sf[(buf * MT + (p * NW + nw) % MT) * 16 + (lane & 15)] =
                     step(round) < steps ? r.sf[p] : 0.0f;
         }
     };
@@ -361,13 +371,25 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int u = 0; u < NT; ++u) total[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](const R &r, int half) {
-        const u32x4 *xl = lds + (half * KS + kg) * F * 64 + lane;
+    // HELD: row m's units (16 channels of bf16 or E4M3 a unit of 16 bytes or, converted, 8) start
+    // at m * pitch, an odd number so that rows lie in different banks; behind the rows
+    // the zeros that steps behind the last read, and the scales.
+    constexpr int kStepUnits = 4 * U;
+    const int pitch = steps * kStepUnits + 1, zeros = per * pitch;
+    float *const held_sf = reinterpret_cast<float *>(all + zeros + kStepUnits);
+    const int my_row = (lane & 15) < pass.rows ? lane & 15 : pass.rows - 1;
+    auto compute = [&](const R &r, int half, int round) {
+        const int s = step(round);
+        const u32x4 *xl = HELD ? all + (s < steps ? my_row * pitch + s * kStepUnits : zeros) +
+                                     (MX && !FP8 ? 4 * q : q)
+                               : lds + (half * KS + kg) * F * 64 + lane;
+        constexpr int kUnit = !HELD ? 64 : MX && !FP8 ? 1 : 4;      // from one unit to the next
         float sx[MT];
         if (FP8)
 #pragma unroll
             for (int t = 0; t < MT; ++t)
-                sx[t] = lds_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)];
+                sx[t] = !HELD ? ring_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)]
+                        : s < steps ? held_sf[my_row * steps + s] : 0.0f;
 #pragma unroll
         for (int g = 0; g < P; ++g) {
             constexpr int J = U / P;
@@ -376,7 +398,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int j = 0; j < J; ++j) xs[t][j] = xl[(t * U + g * J + j) * 64];
+                for (int j = 0; j < J; ++j) xs[t][j] = xl[(t * U + g * J + j) * kUnit];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 f32x4 from = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -432,20 +454,40 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     // While a round is computed on, the weights of the next D - 1 are on their way
     // into registers, and their x into registers and then LDS.
     X x[D];
+    if (HELD) {
+        const int tid = threadIdx.x;
+        for (int m = 0; m < pass.rows; ++m) {
+            const int64_t from = row_of(m);
+            const char *row = static_cast<const char *>(a.x) + from * a.k * (FP8 ? 1 : 2);
+#pragma unroll 4
+            for (int u = tid; u < steps * kStepUnits; u += kW4Threads)
+                all[m * pitch + u] =
+                    FP8 && !DIRECT ? e4m3_bf16(reinterpret_cast<const u32x2 *>(row)[u])
+                                   : reinterpret_cast<const u32x4 *>(row)[u];
+            if (FP8)
+                for (int s = tid; s < steps; s += kW4Threads)
+                    held_sf[m * steps + s] = load_scale(a.sf.p, a.sf.ts, a.sf.hs, from, s,
+                                                        a.sf.ue8m0);
+        }
+        if (tid < kStepUnits) all[zeros + tid] = u32x4{0u, 0u, 0u, 0u};
+    } else {
 #pragma unroll
-    for (int d = 0; d + 1 < D; ++d) load_x(x[d], d);
-    store_x(x[0], 0, 0);
+        for (int d = 0; d + 1 < D; ++d) load_x(x[d], d);
+        store_x(x[0], 0, 0);
+    }
     lds_barrier();
     for (int round = 0; round < rounds;) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            load_x(x[(d + D - 1) % D], round + D - 1);
+            if (!HELD) load_x(x[(d + D - 1) % D], round + D - 1);
             load_w(w[(d + D - 1) % D], round + D - 1);
             __builtin_amdgcn_sched_barrier(0);
-            compute(w[d], d);
+            compute(w[d], d, round);
             __builtin_amdgcn_sched_barrier(0);
-            store_x(x[(d + 1) % D], round + 1, (d + 1) % D);
-            lds_barrier();
+            if (!HELD) {
+                store_x(x[(d + 1) % D], round + 1, (d + 1) % D);
+                lds_barrier();
+            }
             if (++round == rounds) break;
         }
     }
@@ -480,23 +522,43 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
         }
 }
 
-template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D>
-hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t stream) {
+template <int FMT, int GROUP, bool FP8, int NT, int MT, int KS, int D, bool HELD = false>
+hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t stream,
+                     int per = 16 * MT, int held_bytes = 0) {
     constexpr int per_block = NT * (kW4Waves / KS);
     const int groups = ((a.n + 15) / 16 + per_block - 1) / per_block;
     // no more passes than these: every expert's last one may be partly filled
-    const int64_t passes = active + slots / (16 * MT);
+    const int64_t passes = active + slots / per;
     // a launch holds fewer than 2^32 threads, and 2^16 blocks along y
     int64_t most = (int64_t(1) << 23) / groups;
     most = most < 1 ? 1 : most > 32768 ? 32768 : most;
     for (int64_t p = 0; p < passes; p += most) {
         const dim3 grid(groups, static_cast<uint32_t>(passes - p < most ? passes - p : most));
-        w4_kernel<FMT, GROUP, FP8, NT, MT, KS, D><<<grid, kW4Threads, 0, stream>>>(
-            a, static_cast<int>(p));
+        w4_kernel<FMT, GROUP, FP8, NT, MT, KS, D, HELD>
+            <<<grid, kW4Threads, held_bytes, stream>>>(a, static_cast<int>(p), per);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+constexpr int kHeldBytes = 64 * 1024;            // two blocks a compute unit
+
+// LDS of a pass of `per` rows held whole, room for the sums of the waves at least.
+int held_bytes(int per, int steps, int tiles_a_wave, bool direct, bool fp8) {
+    const int units = direct ? 8 : 16;
+    const int64_t x = 16 * (per * (int64_t(steps) * units + 1) + units) +
+                      (fp8 ? int64_t(4) * per * steps : 0);
+    const int sums = 16 * kW4Waves * tiles_a_wave * 64;
+    return x > kHeldBytes ? kHeldBytes + 1 : x > sums ? static_cast<int>(x) : sums;
+}
+
+template <int FMT, int GROUP, bool FP8, int NT, int D>
+hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
+                       hipStream_t stream) {
+    return launch_w4<FMT, GROUP, FP8, NT, 1, 4, D, true>(
+        a, active, slots, stream, per,
+        held_bytes(per, a.k / 128, NT, FMT == EP_W4_MXFP4 && FP8, FP8));
 }
 
 // Tile and split, by the sizes that the host knows (us at 64 experts unless said).
@@ -505,18 +567,25 @@ hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t
 //   4096 x 7168: 161 (16) and 195 (32) at 8 rows an expert on average, 225 and 193 at 16; so
 //   32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4 rows, 215 and 165
 //   at 16; so 32 beyond 6.  64 rows gave nothing (16 experts of 64 rows: 150 against 135).
-//   Outputs a wave and waves a group: the widest that leaves 384 blocks, one and a
-//   half a compute unit.  One token of 8 experts (4096 x 7168, 2048 tiles): 24.0
+//   Up to one row an expert on average (EP_W4_INT4: two) x is held, in passes of up to four
+//   rows, while it takes at most 64 KB; an expert with more rows reads its weights again, which is the
+//   cost: EP_W4_INT4 153 without and 143 with at 2 rows, 183 and 201 at 4;
+//   EP_W4_MXFP4 97.4 and 96.5 at one, 132 and 136 at two.  Four waves a group, 64 outputs a
+//   wave or, below 1024 tiles, 32 (of 8 experts' 2048 outputs: 13.4 and 13.5; 512: 11.1 and
+//   8.9).
+//   Otherwise, outputs a wave and waves a group: the widest that leaves 384 blocks, one and a
+//   half a compute unit.  8 experts of one row (4096 x 7168, 2048 tiles): 24.0
 //   with two waves a group of 32 outputs, 30.3 with one, 47.0 with 64 outputs a wave;
 //   26 experts with rows: 73.9, 74.7 and 71.4; 2 experts of 1024 outputs: 8.5 with
 //   four waves a group, 10.8 with two; but every wave has two steps at least (two steps,
-//   16 experts of 512 outputs: 4.6 with one wave a group, 5.5 with four).  Short rows leave a block little to do between
-//   its first and last loads, which more blocks a compute unit hide: 64 outputs a wave
-//   from 32 steps on only (7168 x 2048, 16 steps: 88 with 64, 81 with 32 outputs).
+//   16 experts of 512 outputs: 4.6 with one wave a group, 5.5 with four).  Short rows
+//   leave a block little to do between its first and last loads, which more blocks a
+//   compute unit hide: 64 outputs a wave from 32 steps on only (7168 x 2048, 16 steps:
+//   88 with 64, 81 with 32 outputs).
 //   Three steps in registers instead of two keep more of the weights in flight where a
-//   block is short of waves (one token: 25.7 -> 23.9) or a step is long (64 outputs of
-//   32 rows: 204 -> 197 at 16 rows an expert; not with groups of 32 or 64, whose scales
-//   leave too few registers: 249 -> 285).
+//   block is short of waves (8 experts of one row: 25.7 -> 23.9) or a step is long (64
+//   outputs of 32 rows: 204 -> 197 at 16 rows an expert; not with groups of 32 or 64, whose
+//   scales leave too few registers: 249 -> 285).
 template <int FMT, int GROUP, bool FP8>
 hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk;
@@ -525,13 +594,19 @@ hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     const bool wide = slots > (FMT == EP_W4_MXFP4 ? 6 : 12) * static_cast<int64_t>(a.num_experts);
     constexpr int64_t kBlocks = 384;
     constexpr int deep = FMT == EP_W4_MXFP4 || GROUP == 128 ? 3 : 2;
-    if (tiles >= 16 * kBlocks && a.k >= 32 * 128)
+    const int steps = a.k / 128;
+    const int per = a.num_tokens < 4 ? a.num_tokens : 4;
+    if (slots <= (FMT == EP_W4_MXFP4 ? 1 : 2) * static_cast<int64_t>(a.num_experts) &&
+        steps >= 4 &&
+        held_bytes(per, steps, 4, FMT == EP_W4_MXFP4 && FP8, FP8) <= kHeldBytes)
+        return tiles >= 1024 ? launch_held<FMT, GROUP, FP8, 4, 2>(a, active, slots, per, stream)
+                             : launch_held<FMT, GROUP, FP8, 2, 3>(a, active, slots, per, stream);
+    if (tiles >= 16 * kBlocks && steps >= 32)
         return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, deep>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);
     if (tiles >= 8 * kBlocks)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
-    const int steps = a.k / 128;
     if (steps < 4)
         return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);

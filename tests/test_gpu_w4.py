@@ -331,3 +331,63 @@ def test_offsets_past_32_bits():
         tol = want.abs() * ref.BF16 + x64.abs() @ w64[e].abs().t() * 66 * ref.F32
         ref.assert_close(y[part], want, tol, f"expert {e}")
     assert not bool(y[:rows - 90].any())
+
+
+FEW = [  # T, K, E, k, n, format, group, x, token rows, all on one expert
+    (1, 8, 64, 640, 2064, INT4, 128, "bf16", True, False),
+    (1, 8, 64, 512, 2064, MX, 32, "bf16", True, False),
+    (1, 8, 64, 896, 2064, MX, 32, "f32", True, False),
+    (2, 4, 16, 1152, 104, INT4, 64, "f32", False, False),
+    (4, 4, 16, 768, 24, INT4, 32, "ue8m0", True, False),
+    (4, 4, 16, 1280, 8, MX, 32, "ue8m0", False, False),
+    (16, 1, 16, 640, 40, INT4, 32, "bf16", False, True),
+    (13, 1, 13, 1664, 40, MX, 32, "f32", False, True),
+    (13, 1, 13, 640, 2064, MX, 32, "bf16", True, True),
+    (32, 1, 16, 512, 1040, INT4, 128, "bf16", True, False),
+    (4, 1, 4, 8064, 16, INT4, 128, "bf16", False, True),
+    (4, 1, 4, 8192, 16, INT4, 128, "bf16", False, True),
+    (1, 1, 2, 32768, 16, MX, 32, "f32", True, False),
+    (2, 1, 2, 30720, 16, MX, 32, "f32", True, False),
+    (2, 1, 2, 32768, 16, MX, 32, "f32", True, True),
+    (1, 1, 1, 32640, 24, INT4, 64, "bf16", True, False),
+]
+
+
+@pytest.mark.parametrize("T,K,E,k,n,fmt,group,kind,token_rows,one", FEW)
+def test_few_rows(T, K, E, k, n, fmt, group, kind, token_rows, one):
+    """A row or two an expert, more on some of them; rows as long as may be held and
+    longer; step counts that four waves do not share evenly."""
+    say("few", T, K, E, k, n, fmt, group, kind, token_rows, one)
+    gen = _gen(T + k + n)
+    idx = ref.ids(T, K, E, gen, "cuda", 0.0)
+    if one:
+        idx = torch.full_like(idx, E - 1)
+    h = ep.Handle(T, K, E, 1)
+    h.layout(idx)
+    codes, scales = ref.random_w4(E, n, k, fmt, group, gen, "cuda")
+    x, sf, x64 = _x(T if token_rows else h.capacity, k, kind, gen)
+    out = ref.poisoned((h.capacity, n), torch.bfloat16)
+    h.expert_w4(x, ep.pack_w4(codes, scales), sf=sf, token_rows=token_rows, out=out)
+    _check(h, idx, x64, ref.w4_values(codes, scales, group), _scales64(scales, group, fmt), out,
+           token_rows, "few rows")
+
+
+@pytest.mark.parametrize("fmt,group,kind", [(INT4, 128, "bf16"), (INT4, 32, "f32"),
+                                            (MX, 32, "bf16"), (MX, 32, "f32")])
+def test_few_rows_with_nan(fmt, group, kind):
+    """Rows of one pass, one of them spoilt, and an expert whose weights are."""
+    T, E, k, n = 6, 8, 640, 48
+    gen = _gen(12)
+    codes, scales = ref.random_w4(E, n, k, fmt, group, gen, "cuda")
+    idx = torch.tensor([[2], [2], [2], [2], [2], [5]], device="cuda")
+    h = ep.Handle(T, 1, E, 1)
+    h.layout(idx)
+    x, sf, _ = _x(T, k, kind, gen)
+    want = h.expert_w4(x, ep.pack_w4(codes, scales), sf=sf, token_rows=True)
+    bad = x.clone()
+    bad[1, 600] = float("nan") if kind == "bf16" else 0x7F
+    scales = scales.clone()
+    scales[5, :, -1] = float("nan") if fmt == INT4 else 255
+    got = h.expert_w4(bad, ep.pack_w4(codes, scales), sf=sf, token_rows=True)
+    assert torch.equal(got[[0, 2, 3, 4]], want[[0, 2, 3, 4]])
+    assert bool(got[1].isnan().all()) and bool(got[5].isnan().all())

@@ -180,7 +180,7 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs
                 const float whole = silu * u[j];
                 total = __builtin_fmaf(gh[j], whole, total);
                 const float wg = w * gh[j];
-                    const float slope = s * __builtin_fmaf(g[j], 1.0f - s, 1.0f);
+                const float slope = s * __builtin_fmaf(g[j], 1.0f - s, 1.0f);
                 og[j] = wg * u[j] * slope;
                 ou[j] = wg * silu;
                 oh[j] = w * whole;

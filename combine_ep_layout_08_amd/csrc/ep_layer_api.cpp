@@ -14,6 +14,21 @@ ep_status hip_status(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_HIP
 
 bool known_format(ep_sf_format fmt) { return fmt == EP_SF_F32 || fmt == EP_SF_UE8M0; }
 
+// Whether an output and another buffer, both rows of the given bytes, share memory: then
+// a row's block would read what another has written.  `same`: the two may start at the same
+// address, where each thread reads a place before it writes it.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+bool clash(Span out, Span other, bool same = false) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p),
+                    b = reinterpret_cast<uintptr_t>(other.p);
+    if (!a || !b || (same && a == b)) return false;
+    return a < b + other.bytes && b < a + out.bytes;
+}
+
 // A handle from ep_handle_init (or a plain copy of one) that has a layout.
 ep_status handle_status(const ep_handle *h) {
     if (!h) return EP_ERR_NULL;
@@ -84,6 +99,12 @@ ep_status ep_add_rmsnorm(const void *x, const void *residual, const void *weight
         !aligned(out_z, 16) || !aligned(out_y, 16) || !aligned(out_q, 16) ||
         !aligned(out_rstd, 4))
         return EP_ERR_MISALIGNED;
+    const int64_t codes = static_cast<int64_t>(num_tokens) * hidden;
+    const Span ins[] = {{x, 2 * codes}, {residual, 2 * codes}};
+    const Span zs{out_z, 2 * codes}, ys{out_y, 2 * codes}, qs{out_q, codes};
+    for (const Span &in : ins)
+        if (clash(zs, in, true) || clash(ys, in) || clash(qs, in)) return EP_ERR_UNSUPPORTED;
+    if (clash(ys, zs) || clash(qs, zs) || clash(qs, ys)) return EP_ERR_UNSUPPORTED;
     a.x = x;
     a.residual = residual;
     a.weight = weight;
@@ -119,6 +140,11 @@ ep_status ep_add_rmsnorm_backward(const void *grad_y, const void *z, const void 
         return EP_ERR_MISALIGNED;
     if (num_tokens > 0 && (!grad_y || !z || !weight || !rstd || (!grad_x && !grad_weight)))
         return EP_ERR_NULL;
+    const int64_t bytes = 2 * static_cast<int64_t>(num_tokens) * hidden;
+    const Span gx{grad_x, bytes};
+    if (clash(gx, {grad_y, bytes}, true) || clash(gx, {z, bytes}, true) ||
+        clash(gx, {grad_z, bytes}, true))
+        return EP_ERR_UNSUPPORTED;
     const size_t need = grad_weight ? ep_add_rmsnorm_backward_workspace(num_tokens, hidden) : 0;
     if (need > 0 && (!workspace || ws_bytes < need)) return EP_ERR_WORKSPACE;
     ep::NormGradArgs a{};
@@ -185,6 +211,9 @@ ep_status ep_expert_w4(const ep_handle *h, const void *x, ep_dtype x_dtype, int3
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16))
         return EP_ERR_MISALIGNED;
     if (!rows) return EP_OK;
+    const int64_t x_rows = token_rows ? h->num_tokens : h->capacity;
+    if (clash({out, 2 * int64_t(h->capacity) * n}, {x, x_rows * k * (fp8 ? 1 : 2)}))
+        return EP_ERR_UNSUPPORTED;
     a.counts = h->counts;
     a.psum = h->psum;
     a.src_meta = h->src_meta;
@@ -238,6 +267,9 @@ ep_status ep_swiglu(const ep_handle *h, const void *gate_up, int32_t inter,
         !aligned(saved, 16))
         return EP_ERR_MISALIGNED;
     if (!rows) return EP_OK;
+    const int64_t part = static_cast<int64_t>(h->capacity) * inter;
+    const Span in{gate_up, 4 * part}, hs{out_h, part * (h_fp8 ? 1 : 2)}, ss{saved, 2 * part};
+    if (clash(hs, in) || clash(ss, in) || clash(ss, hs)) return EP_ERR_UNSUPPORTED;
     a.dst = h->dst_slot;
     a.scalars = h->scalars;
     a.num_slots = static_cast<int64_t>(h->num_tokens) * h->num_topk;
@@ -277,6 +309,12 @@ ep_status ep_swiglu_backward(const ep_handle *h, const void *grad_h, int32_t int
         !aligned(grad_gate_up, 16) || !aligned(grad_row_weights, 4) || !aligned(out_h, 16))
         return EP_ERR_MISALIGNED;
     if (!rows) return EP_OK;
+    const int64_t part = static_cast<int64_t>(h->capacity) * inter;
+    const Span gh{grad_h, 2 * part}, in{saved, part * (fp8 ? 2 : 4)};
+    const Span gg{grad_gate_up, 4 * part}, hs{out_h, 2 * part};
+    if (clash(gg, gh) || clash(gg, in, !fp8) || clash(hs, gh, true) || clash(hs, in) ||
+        clash(hs, gg))
+        return EP_ERR_UNSUPPORTED;
     a.dst = h->dst_slot;
     a.scalars = h->scalars;
     a.num_slots = static_cast<int64_t>(h->num_tokens) * h->num_topk;

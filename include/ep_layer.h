@@ -24,7 +24,9 @@
  * on expert rows take a handle that has been laid out (ep.h), touch only
  * rows that hold a slot (gap rows and rows at or past psum[E] are neither
  * read nor written) and, like dispatch, do nothing after a capacity or
- * timeout error on the handle.  bf16 rounding is to nearest, ties to even.
+ * timeout error on the handle.  An output overlaps no input and no other output
+ * but where it is said that it may be one (of the row buffers such calls are refused with
+ * EP_ERR_UNSUPPORTED).  bf16 rounding is to nearest, ties to even.
  * ep_time_next_call does not apply to these calls.
  *
  * E4M3 rows ("codes") and their scales are those of ep_quantize_fp8: blocks of
@@ -75,7 +77,7 @@ ep_status ep_add_rmsnorm(const void *x, const void *residual, const void *weight
  *   grad_z      NULL or bf16 [num_tokens, hidden]: the gradient that reaches z
  *               on its other way, along the residual.
  *   grad_x      NULL or bf16 [num_tokens, hidden]: gradient of x and of the
- *               residual (they share it); may be grad_y or grad_z itself.
+ *               residual (they share it); may be grad_y, grad_z or z itself.
  *   grad_weight NULL or fp32 [hidden], summed in binary32 in a fixed order
  *               (zeros when num_tokens is 0).
  *   workspace   device, 16-byte aligned, ep_add_rmsnorm_backward_workspace bytes;

@@ -314,3 +314,15 @@ def test_two_streams():
         for a, b in zip(got, want):
             for u, v in zip(a, b):
                 assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("T", [3, 700, 1500])
+def test_backward_over_z(T):
+    gen = _gen(14)
+    H = 1024
+    z, w = _rows(T, H, gen), _weight(H, gen, torch.bfloat16)
+    g = _rows(T, H, gen)
+    rstd = ep.add_rmsnorm(z, w, want_rstd=True)[4]
+    want = ep.add_rmsnorm_backward(g, z, w, rstd)
+    got = ep.add_rmsnorm_backward(g, z, w, rstd, grad_x=z)
+    assert got[0] is z and torch.equal(z, want[0]) and torch.equal(got[1], want[1])

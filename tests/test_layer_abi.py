@@ -398,3 +398,34 @@ def test_status_becomes_an_error(fake):
     with pytest.raises(ep.EpError) as e:
         ep.add_rmsnorm(_bf16(2, 256), torch.ones(256))
     assert e.value.status == ep.EP_ERR_HIP
+
+
+FAR = A16 + (1 << 30)                    # nothing of these sizes reaches from A16 to there
+
+
+@pytest.mark.parametrize("call", [
+    lambda: norm(y=A16),                                        # y over x
+    lambda: norm(r=FAR, y=FAR),
+    lambda: norm(y=FAR, z=FAR),
+    lambda: norm(z=A16 + 16, y=None),                           # z over a part of x
+    lambda: norm(y=None, q=A16 + 4 * 512 - 16, sf=FAR),         # codes over x's end
+    lambda: norm(y=FAR, q=FAR + 4 * 512 - 16, sf=FAR),
+    lambda: norm(z=FAR, y=None, q=FAR, sf=FAR),
+    lambda: norm_grad(gx=A16 + 16),
+    lambda: norm_grad(g=FAR, gx=FAR - 16),
+    lambda: norm_grad(g=FAR, z=FAR, gz=A16 + 16),
+    lambda: w4(),
+    lambda: w4(**FP8),
+    lambda: w4(tokens=1, x=A16 + 16),
+    lambda: act(),
+    lambda: act(hdt=ep.EP_FP8_E4M3, sf=FAR),
+    lambda: act(out=FAR, saved=A16, ssf=FAR),
+    lambda: act(out=FAR, saved=FAR, ssf=FAR),
+    lambda: act_grad(),
+    lambda: act_grad(saved=FAR, ggu=FAR + 16),
+    lambda: act_grad(saved=FAR, ggu=FAR + (1 << 28), out=FAR),
+    lambda: act_grad(saved=FAR, ggu=FAR, out=FAR),
+    lambda: act_grad(saved=FAR, dt=ep.EP_FP8_E4M3, sf=A16, ggu=FAR),
+])
+def test_overlapping_rows_are_refused(call):
+    assert call() == ep.EP_ERR_UNSUPPORTED

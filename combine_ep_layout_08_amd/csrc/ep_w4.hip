@@ -4,7 +4,7 @@
 // out[r, :] = x[r, :] . W[e]^T for the rows r of expert e, as matrix
 // instructions of 16 rows x 16 outputs x 32 channels (v_mfma_f32_16x16x32_bf16;
 // lane l holds row l % 16 of x, output l % 16 of W, channels 8 (l / 16) .. + 7 of
-// each, and accumulates rows 4 (l / 16) .. + 3 of output l % 16).
+// each, and accumulates four of operand A's for one of operand B's).
 //
 // Packed weights: for every expert, tile of 16 outputs and step of 128
 // channels, one record of 1 KB: lane l's 16 bytes at 16 l, dword j eight codes of
@@ -193,10 +193,16 @@ __device__ inline f32x4 mfma_mx(u32x4 w, uint32_t scale, u32x4 x0, u32x4 x1, f32
 // What a wave has read of its weights for one step: NT records and their scales.
 template <int FMT, int GROUP, int NT>
 struct Records {
-    static constexpr int kScaleWords = FMT == EP_W4_MXFP4 ? 1 : 256 / GROUP;
+    static constexpr int kScaleWords = FMT == EP_W4_MXFP4 || GROUP > 32 ? 1 : 2;
     u32x4 w[NT];
     uint32_t sw[NT][kScaleWords];
 };
+
+// The value of the other lane of an even and an odd one.
+__device__ inline uint32_t other_of_pair(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, true));
+}
 
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
@@ -210,9 +216,13 @@ constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
 
 // One block for one pass (MT tiles of 16 rows of one expert) and NW groups of NT
 // tiles of 16 outputs: a group is one wave's, or KS waves take every KS-th step
-// each and add up through LDS.  The weights are operand A and x operand B, so a
-// lane holds outputs 4 (l / 16) .. + 3 of row l % 16: one scale of x a lane, the weights'
-// scales of its four outputs consecutive, and 8-byte stores.
+// each and add up through LDS.
+//   EP_W4_INT4: x is operand A and the weights operand B, so a lane has the sums of four rows
+//   of one output and a group's sums one scale of the weights a lane.  (The other way
+//   round, four scales a lane and group had to be unpacked and held: groups of 32, 64 outputs
+//   of 32 rows spilled registers; 128 tokens 250 -> 219 us with groups of 32, 4 tokens 78 -> 69.)
+//   EP_W4_MXFP4: the other way round, so a lane has four outputs of one row, one scale of x,
+//   and stores 8 bytes; the weights' scales are the instructions' business.
 //   x is brought by the block's waves together and handed over through LDS, in
 //   the lanes' order (16 bytes a lane, no bank conflicts): loads of 16 rows by 64
 //   bytes keep the address units busy for about 35 cycles each, as long as 400
@@ -239,7 +249,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     constexpr int kXUnits = HELD ? 1 : D * KS * F * 64;
     constexpr int kSumUnits = KS == 1 || HELD ? 0 : kW4Waves * NT * MT * 64;
     __shared__ u32x4 ring[kXUnits > kSumUnits ? kXUnits : kSumUnits];
-    __shared__ float ring_sf[FP8 && !HELD ? D * KS * MT * 16 : 1];
+    alignas(16) __shared__ float ring_sf[FP8 && !HELD ? D * KS * MT * 16 : 1];
     extern __shared__ u32x4 all[];               // HELD: x, then the sums
     u32x4 *const lds = HELD ? all : ring;
     const int lane = threadIdx.x & 63, q = lane >> 4;
@@ -252,7 +262,8 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     asm("" : "+s"(mask));
     asm("" : "+v"(one28));
 
-    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, per, lane);
+    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, per,
+                                lane);
     if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
     // The group's records are consecutive; tiles behind the last are read as the
     // last and not stored.
@@ -265,7 +276,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     const Buffer scales = bounded(static_cast<const char *>(a.scales) + record * kScaleStep,
                                   mine * steps * kScaleStep);
     uint32_t code_at = 16 * lane;
-    uint32_t scale_at = MX ? lane : 8 * P * q;
+    uint32_t scale_at = MX ? lane : 2 * P * (lane & 15);
     const int rounds = (steps + KS - 1) / KS;
     auto step = [&](int round) { return round * KS + kg; };
     auto held = [&](int s) { return s < steps ? s : steps - 1; };
@@ -281,17 +292,13 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
             if (MX) {
                 r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b8(scales, scale_at, sat, 0);
             } else if (P == 1) {
+                r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b16(scales, scale_at, sat, 0);
+            } else if (P == 2) {
+                r.sw[t][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, scale_at, sat, 0);
+            } else {
                 const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(scales, scale_at, sat, 0);
                 r.sw[t][0] = v.x;
                 r.sw[t][1 % R::kScaleWords] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < R::kScaleWords / 4; ++i) {
-                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
-                        scales, scale_at + 16 * i, sat, 0);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r.sw[t][(4 * i + k) % R::kScaleWords] = v[k];
-                }
             }
         }
         if (round + 1 >= rounds) code_at = scale_at = kNowhere;
@@ -384,12 +391,22 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
                                      (MX && !FP8 ? 4 * q : q)
                                : lds + (half * KS + kg) * F * 64 + lane;
         constexpr int kUnit = !HELD ? 64 : MX && !FP8 ? 1 : 4;      // from one unit to the next
-        float sx[MT];
+        f32x4 sx[MT];                            // of the rows that a lane has sums of
         if (FP8)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                sx[t] = !HELD ? ring_sf[((half * KS + kg) * MT + t) * 16 + (lane & 15)]
-                        : s < steps ? held_sf[my_row * steps + s] : 0.0f;
+            for (int t = 0; t < MT; ++t) {
+                const float *ring_at = ring_sf + ((half * KS + kg) * MT + t) * 16;
+                if (MX) {
+                    sx[t][0] = !HELD ? ring_at[lane & 15]
+                               : s < steps ? held_sf[my_row * steps + s] : 0.0f;
+                } else if (!HELD) {
+                    sx[t] = *reinterpret_cast<const f32x4 *>(ring_at + 4 * q);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sx[t][i] = s < steps ? held_sf[(i < pass.rows ? i : 0) * steps + s] : 0.0f;
+                }
+            }
 #pragma unroll
         for (int g = 0; g < P; ++g) {
             constexpr int J = U / P;
@@ -405,8 +422,8 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
                 if (!MX)
 #pragma unroll
                     for (int j = 0; j < J; ++j)
-                        from = mfma(u32x4{kMinus136, kMinus136, kMinus136, kMinus136},
-                                    xs[t][j], from);
+                        from = mfma(xs[t][j],
+                                    u32x4{kMinus136, kMinus136, kMinus136, kMinus136}, from);
 #pragma unroll
                 for (int u = 0; u < NT; ++u) acc[t][u] = MX && !FP8 ? total[t][u] : from;
             }
@@ -427,28 +444,27 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
                                            : int4_plus128(w4, mask, one28);
 #pragma unroll
                         for (int t = 0; t < MT; ++t)
-                            acc[t][u] = mfma(w, xs[t][j], acc[t][u]);
+                            acc[t][u] = MX ? mfma(w, xs[t][j], acc[t][u])
+                                           : mfma(xs[t][j], w, acc[t][u]);
                     }
             }
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int u = 0; u < NT; ++u) {
+                const uint32_t sw = r.sw[u][g / 2 % R::kScaleWords];
+                const float f = MX ? 1.0f : g & 1 ? bf16_hi(sw) : bf16_lo(sw);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f = 1.0f;
-                    if (!MX) {
-                        const uint32_t sw = r.sw[u][(i * P + g) / 2 % R::kScaleWords];
-                        f = (i * P + g) & 1 ? bf16_hi(sw) : bf16_lo(sw);
+                for (int t = 0; t < MT; ++t) {
+                    if (MX && !FP8) {
+                        total[t][u] = acc[t][u];
+                        continue;
                     }
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        if (MX && !FP8) {
-                            total[t][u][i] = acc[t][u][i];
-                            continue;
-                        }
-                        const float m = MX ? sx[t] : FP8 ? f * sx[t] : f;
+                    for (int i = 0; i < 4; ++i) {
+                        const float m = MX ? sx[t][0] : FP8 ? f * sx[t][i] : f;
                         total[t][u][i] = __builtin_fmaf(m, acc[t][u][i], total[t][u][i]);
                     }
                 }
+            }
         }
     };
     // While a round is computed on, the weights of the next D - 1 are on their way
@@ -514,11 +530,28 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
                     v += __builtin_bit_cast(
                         f32x4, lds[(((nw * KS + k) * MT + t) * NT + u) * 64 + lane]);
             }
-            const int m = 16 * t + (lane & 15), col = (tile0 + u) * 16 + 4 * q;
-            if (m < pass.rows && col < a.n)
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) +
-                                           static_cast<int64_t>(pass.start + m) * a.n + col) =
-                    u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+            uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<int64_t>(pass.start) * a.n;
+            const uint32_t lo = pack2(v[0], v[1]), hi = pack2(v[2], v[3]);
+            if (MX) {
+                const int m = 16 * t + (lane & 15), col = (tile0 + u) * 16 + 4 * q;
+                if (m < pass.rows && col < a.n)
+                    *reinterpret_cast<u32x2 *>(out + static_cast<int64_t>(m) * a.n + col) =
+                        u32x2{lo, hi};
+                continue;
+            }
+            // two lanes' outputs of a row make a word: the even lane's of rows 0 and 2, the odd
+            // one's of rows 1 and 3
+            const int m = 16 * t + 4 * q + (lane & 1), col = (tile0 + u) * 16 + (lane & 14);
+            const uint32_t pick = lane & 1 ? 0x03020706u : 0x05040100u;
+            const uint32_t first_row = __builtin_amdgcn_perm(other_of_pair(lo), lo, pick);
+            const uint32_t second_row = __builtin_amdgcn_perm(other_of_pair(hi), hi, pick);
+            if (col >= a.n) continue;
+            if (m < pass.rows)
+                *reinterpret_cast<uint32_t *>(out + static_cast<int64_t>(m) * a.n + col) =
+                    first_row;
+            if (m + 2 < pass.rows)
+                *reinterpret_cast<uint32_t *>(out + static_cast<int64_t>(m + 2) * a.n + col) =
+                    second_row;
         }
 }
 
@@ -561,46 +594,50 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
         held_bytes(per, a.k / 128, NT, FMT == EP_W4_MXFP4 && FP8, FP8));
 }
 
-// Tile and split, by the sizes that the host knows (us at 64 experts unless said).
-//   Rows a pass: 16 or 32.  The codes' conversion and the weights' reading are paid once a
-//   pass, an empty half of a wide one costs its matrix instructions.  EP_W4_INT4,
-//   4096 x 7168: 161 (16) and 195 (32) at 8 rows an expert on average, 225 and 193 at 16; so
-//   32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4 rows, 215 and 165
-//   at 16; so 32 beyond 6.  64 rows gave nothing (16 experts of 64 rows: 150 against 135).
+// Tile and split, by the sizes that the host knows (us at 64 experts of 4096 x 7168 and
+// EP_W4_INT4 groups of 128 unless said).
 //   Up to one row an expert on average (EP_W4_INT4: two) x is held, in passes of up to four
-//   rows, while it takes at most 64 KB; an expert with more rows reads its weights again, which is the
-//   cost: EP_W4_INT4 153 without and 143 with at 2 rows, 183 and 201 at 4;
-//   EP_W4_MXFP4 97.4 and 96.5 at one, 132 and 136 at two.  Four waves a group, 64 outputs a
-//   wave or, below 1024 tiles, 32 (of 8 experts' 2048 outputs: 13.4 and 13.5; 512: 11.1 and
-//   8.9).
-//   Otherwise, outputs a wave and waves a group: the widest that leaves 384 blocks, one and a
-//   half a compute unit.  8 experts of one row (4096 x 7168, 2048 tiles): 24.0
-//   with two waves a group of 32 outputs, 30.3 with one, 47.0 with 64 outputs a wave;
-//   26 experts with rows: 73.9, 74.7 and 71.4; 2 experts of 1024 outputs: 8.5 with
-//   four waves a group, 10.8 with two; but every wave has two steps at least (two steps,
-//   16 experts of 512 outputs: 4.6 with one wave a group, 5.5 with four).  Short rows
-//   leave a block little to do between its first and last loads, which more blocks a
-//   compute unit hide: 64 outputs a wave from 32 steps on only (7168 x 2048, 16 steps:
-//   88 with 64, 81 with 32 outputs).
+//   rows, while it takes at most 64 KB; an expert with more rows reads its weights again,
+//   which is the cost: EP_W4_INT4 153 without and 143 with at 2 rows, 183 and 201 at 4;
+//   EP_W4_MXFP4 97.4 and 96.5 at one, 132 and 136 at two.  Four waves a group, 64
+//   outputs a wave or, below 1024 tiles, 32 (8 experts of 2048 outputs: 12.6 and 12.7;
+//   of 512: 10.8 and 8.8).
+//   Otherwise, rows a pass: 16 or 32.  The codes' conversion and the weights' reading are paid
+//   once a pass, an empty half of a wide one costs its matrix instructions.
+//   EP_W4_INT4: 159 (16) and 184 (32) at 8 rows an expert on average, 189 and 189 at 12, 226
+//   and 194 at 16; so 32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4
+//   rows, 215 and 165 at 16; so 32 beyond 6.  64 rows gave nothing (16 experts of 64 rows: 150
+//   against 135).
+//   Outputs a wave and waves a group: the widest that leaves 384 blocks, one and a half a
+//   compute unit, of the passes that there will be at least (with 128 rows for each of 8
+//   experts, that is 32 passes, 90 with 64 outputs and one wave, 105 with 32, 146 with 32 and
+//   two).  26 experts with rows: 73.9 with two waves a group of 32 outputs, 74.7 with one,
+//   71.4 with 64 outputs; 2 experts of 1024 outputs: 8.5 with four waves a group, 10.8 with
+//   two; but every wave has two steps at least (two steps, 16 experts of 512 outputs: 4.6
+//   with one wave a group, 5.5 with four).  Short rows leave a block little to do between
+//   its first and last loads, which more blocks a compute unit hide: 64 outputs a wave
+//   from 32 steps on only (7168 x 2048, 16 steps, groups of 64, 4 rows: 87 with 64, 81 with 32).
 //   Three steps in registers instead of two keep more of the weights in flight where a
-//   block is short of waves (8 experts of one row: 25.7 -> 23.9) or a step is long (64
-//   outputs of 32 rows: 204 -> 197 at 16 rows an expert; not with groups of 32 or 64, whose
-//   scales leave too few registers: 249 -> 285).
+//   block is short of waves (8 experts of one row: 25.7 -> 23.9) or, EP_W4_MXFP4, a step is
+//   long (64 outputs of 32 rows: 173 -> 169 at 16 rows an expert; EP_W4_INT4, which has more
+//   to do a step, 194 and 193, with groups of 32 217 and 228).
 template <int FMT, int GROUP, bool FP8>
 hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
-    const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk;
-    const int64_t active = slots < a.num_experts ? slots : a.num_experts;
-    const int64_t tiles = active * ((a.n + 15) / 16);
-    const bool wide = slots > (FMT == EP_W4_MXFP4 ? 6 : 12) * static_cast<int64_t>(a.num_experts);
+    constexpr bool MX = FMT == EP_W4_MXFP4;
     constexpr int64_t kBlocks = 384;
-    constexpr int deep = FMT == EP_W4_MXFP4 || GROUP == 128 ? 3 : 2;
+    constexpr int deep = MX ? 3 : 2;
+    const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk, experts = a.num_experts;
+    const int64_t active = slots < experts ? slots : experts;
     const int steps = a.k / 128;
     const int per = a.num_tokens < 4 ? a.num_tokens : 4;
-    if (slots <= (FMT == EP_W4_MXFP4 ? 1 : 2) * static_cast<int64_t>(a.num_experts) &&
-        steps >= 4 &&
-        held_bytes(per, steps, 4, FMT == EP_W4_MXFP4 && FP8, FP8) <= kHeldBytes)
-        return tiles >= 1024 ? launch_held<FMT, GROUP, FP8, 4, 2>(a, active, slots, per, stream)
-                             : launch_held<FMT, GROUP, FP8, 2, 3>(a, active, slots, per, stream);
+    if (slots <= (MX ? 1 : 2) * experts && steps >= 4 &&
+        held_bytes(per, steps, 4, MX && FP8, FP8) <= kHeldBytes)
+        return active * ((a.n + 15) / 16) >= 1024
+                   ? launch_held<FMT, GROUP, FP8, 4, 2>(a, active, slots, per, stream)
+                   : launch_held<FMT, GROUP, FP8, 2, 3>(a, active, slots, per, stream);
+    const bool wide = slots > (MX ? 6 : 12) * experts;
+    const int64_t passes = slots / (wide ? 32 : 16);
+    const int64_t tiles = (passes > active ? passes : active) * ((a.n + 15) / 16);
     if (tiles >= 16 * kBlocks && steps >= 32)
         return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, deep>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);

@@ -595,32 +595,36 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
 }
 
 // Tile and split, by the sizes that the host knows (us at 64 experts of 4096 x 7168 and
-// EP_W4_INT4 groups of 128 unless said).
-//   Up to one row an expert on average (EP_W4_INT4: two) x is held, in passes of up to four
-//   rows, while it takes at most 64 KB; an expert with more rows reads its weights again,
-//   which is the cost: EP_W4_INT4 153 without and 143 with at 2 rows, 183 and 201 at 4;
-//   EP_W4_MXFP4 97.4 and 96.5 at one, 132 and 136 at two.  Four waves a group, 64
-//   outputs a wave or, below 1024 tiles, 32 (8 experts of 2048 outputs: 12.6 and 12.7;
-//   of 512: 10.8 and 8.8).
+// EP_W4_INT4 groups of 128 unless said).  A grid is counted in tiles of 16 outputs of
+// the passes that there will be at least; kBlocks is one and a half blocks a compute unit.
+//   Few rows: x is held, in passes of up to four rows, while it takes at most 64 KB.  An expert
+//   with more rows reads its weights again, which is the cost: EP_W4_INT4 153 without and
+//   143 with at 2 rows an expert on average, 183 and 201 at 4; EP_W4_MXFP4 97.4 and 96.5 at
+//   one, 132 and 136 at two (9 tokens, 320 x 4224: 13.4 and 10.8).  Up to four tokens no expert
+//   has more (4 tokens, 8 experts of 2192 x 6272, 2.5 rows: 22.5 and 19.2), and in a small grid
+//   more passes fill the card (8 experts of 360 x 1920, 14 rows: 7.8 and 7.1; no longer with
+//   1320 tiles: 312 x 5888, 33 rows, 14.9 and 17.5).  Four waves a group, 64 outputs a wave or,
+//   below 1920 tiles, 32 (2048 tiles: 22.2 with 64 and 24.3 with 32; 1788 of 5248 channels: 18.0
+//   and 16.8; 256: 10.8 and 8.8).
 //   Otherwise, rows a pass: 16 or 32.  The codes' conversion and the weights' reading are paid
 //   once a pass, an empty half of a wide one costs its matrix instructions.
 //   EP_W4_INT4: 159 (16) and 184 (32) at 8 rows an expert on average, 189 and 189 at 12, 226
 //   and 194 at 16; so 32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4
-//   rows, 215 and 165 at 16; so 32 beyond 6.  64 rows gave nothing (16 experts of 64 rows: 150
-//   against 135).
-//   Outputs a wave and waves a group: the widest that leaves 384 blocks, one and a half a
-//   compute unit, of the passes that there will be at least (with 128 rows for each of 8
-//   experts, that is 32 passes, 90 with 64 outputs and one wave, 105 with 32, 146 with 32 and
-//   two).  26 experts with rows: 73.9 with two waves a group of 32 outputs, 74.7 with one,
-//   71.4 with 64 outputs; 2 experts of 1024 outputs: 8.5 with four waves a group, 10.8 with
-//   two; but every wave has two steps at least (two steps, 16 experts of 512 outputs: 4.6
-//   with one wave a group, 5.5 with four).  Short rows leave a block little to do between
-//   its first and last loads, which more blocks a compute unit hide: 64 outputs a wave
-//   from 32 steps on only (7168 x 2048, 16 steps, groups of 64, 4 rows: 87 with 64, 81 with 32).
+//   rows, 215 and 165 at 16; so 32 beyond 6.  But only where wide passes fill the card too:
+//   EP_W4_INT4 with 2304 tiles (32 experts, 1152 x 2304, 17.6 rows) 23.1 (16) and 25.1;
+//   EP_W4_MXFP4 with 2052 tiles (16 experts, 1824 x 4480, 36 rows) 41.8 and 33.9.  64 rows gave
+//   nothing (16 experts of 64 rows: 150 against 135).
+//   Outputs a wave and waves a group: the widest that fills the card.  Short rows leave a
+//   block little to do between its first and last loads, which more blocks a compute unit
+//   hide: 64 outputs a wave from 32 steps on only (7168 x 2048, 16 steps, groups of 64, 4
+//   rows: 87 with 64, 81 with 32).  Two waves a group below 3072 tiles (16 experts,
+//   712 x 1152: 7.8, one wave 8.5), four below 768 if each has a few steps (8 experts, 312 x 5888:
+//   14.9, two waves 17.5; 1208 x 1664, 13 steps: 9.1 and 7.9); of two or three steps one wave
+//   takes all (16 experts of 512 x 256: 4.6, four waves 5.5).
 //   Three steps in registers instead of two keep more of the weights in flight where a
-//   block is short of waves (8 experts of one row: 25.7 -> 23.9) or, EP_W4_MXFP4, a step is
-//   long (64 outputs of 32 rows: 173 -> 169 at 16 rows an expert; EP_W4_INT4, which has more
-//   to do a step, 194 and 193, with groups of 32 217 and 228).
+//   block is short of waves or, EP_W4_MXFP4, a step is long (64 outputs of 32 rows: 173 -> 169
+//   at 16 rows an expert; EP_W4_INT4, which has more to do a step, 194 and 193, with groups
+//   of 32 217 and 228).
 template <int FMT, int GROUP, bool FP8>
 hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     constexpr bool MX = FMT == EP_W4_MXFP4;
@@ -629,29 +633,28 @@ hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk, experts = a.num_experts;
     const int64_t active = slots < experts ? slots : experts;
     const int steps = a.k / 128;
+    auto tiles_of = [&](int rows) {
+        const int64_t passes = slots / rows;
+        return (passes > active ? passes : active) * ((a.n + 15) / 16);
+    };
     const int per = a.num_tokens < 4 ? a.num_tokens : 4;
-    if (slots <= (MX ? 1 : 2) * experts && steps >= 4 &&
-        held_bytes(per, steps, 4, MX && FP8, FP8) <= kHeldBytes)
-        return active * ((a.n + 15) / 16) >= 1024
+    const bool few = a.num_tokens <= 4 || 2 * slots <= (MX ? 3 : 4) * experts ||
+                     tiles_of(4) <= 2 * kBlocks;
+    if (few && steps >= 4 && held_bytes(per, steps, 4, MX && FP8, FP8) <= kHeldBytes)
+        return tiles_of(per) >= 5 * kBlocks
                    ? launch_held<FMT, GROUP, FP8, 4, 2>(a, active, slots, per, stream)
                    : launch_held<FMT, GROUP, FP8, 2, 3>(a, active, slots, per, stream);
-    const bool wide = slots > (MX ? 6 : 12) * experts;
-    const int64_t passes = slots / (wide ? 32 : 16);
-    const int64_t tiles = (passes > active ? passes : active) * ((a.n + 15) / 16);
+    const bool wide = slots > (MX ? 6 : 12) * experts && tiles_of(32) >= (MX ? 4 : 8) * kBlocks;
+    const int64_t tiles = tiles_of(wide ? 32 : 16);
     if (tiles >= 16 * kBlocks && steps >= 32)
         return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, deep>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);
-    if (tiles >= 8 * kBlocks)
-        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
-                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
-    if (steps < 4)
-        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream)
-                    : launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
-    if (tiles >= 4 * kBlocks || steps < 8)
-        return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 2, 2>(a, active, slots, stream)
-                    : launch_w4<FMT, GROUP, FP8, 2, 1, 2, 3>(a, active, slots, stream);
-    return wide ? launch_w4<FMT, GROUP, FP8, 2, 2, 4, 2>(a, active, slots, stream)
-                : launch_w4<FMT, GROUP, FP8, 2, 1, 4, 3>(a, active, slots, stream);
+    if (wide) return launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream);
+    if (tiles >= 8 * kBlocks || steps < 4)
+        return launch_w4<FMT, GROUP, FP8, 2, 1, 1, 2>(a, active, slots, stream);
+    return tiles >= 2 * kBlocks || steps < 14
+               ? launch_w4<FMT, GROUP, FP8, 2, 1, 2, 2>(a, active, slots, stream)
+               : launch_w4<FMT, GROUP, FP8, 2, 1, 4, 3>(a, active, slots, stream);
 }
 
 template <int FMT, int GROUP>

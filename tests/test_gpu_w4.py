@@ -391,3 +391,33 @@ def test_few_rows_with_nan(fmt, group, kind):
     got = h.expert_w4(bad, ep.pack_w4(codes, scales), sf=sf, token_rows=True)
     assert torch.equal(got[[0, 2, 3, 4]], want[[0, 2, 3, 4]])
     assert bool(got[1].isnan().all()) and bool(got[5].isnan().all())
+
+
+SPLITS = [  # T, K, E, k, n, format, group, x: every tile and split that the sizes may choose
+    (20, 4, 8, 2304, 1248, INT4, 32, "bf16"),       # two waves a group
+    (20, 4, 8, 2304, 304, INT4, 64, "f32"),         # four waves a group
+    (24, 3, 6, 2048, 904, MX, 32, "ue8m0"),
+    (64, 2, 8, 1152, 6200, INT4, 32, "ue8m0"),      # one wave a group, 16 and 32 rows
+    (128, 2, 8, 1152, 6200, INT4, 32, "f32"),
+    (128, 2, 8, 1152, 6200, MX, 32, "f32"),
+    (64, 2, 16, 4224, 6184, INT4, 64, "bf16"),      # 64 outputs a wave
+    (130, 2, 16, 4224, 6184, INT4, 64, "f32"),
+    (130, 2, 16, 4224, 6184, MX, 32, "bf16"),
+    (9, 4, 4, 640, 72, INT4, 128, "f32"),           # a small grid, rows held
+    (4, 6, 8, 1024, 72, MX, 32, "f32"),             # few tokens, more rows an expert than one
+]
+
+
+@pytest.mark.parametrize("T,K,E,k,n,fmt,group,kind", SPLITS)
+def test_tiles_and_splits(T, K, E, k, n, fmt, group, kind):
+    say("splits", T, K, E, k, n, fmt, group, kind)
+    gen = _gen(T + k + n)
+    idx = ref.ids(T, K, E, gen, "cuda", 0.0)
+    h = ep.Handle(T, K, E, 8)
+    h.layout(idx)
+    codes, scales = ref.random_w4(E, n, k, fmt, group, gen, "cuda")
+    x, sf, x64 = _x(h.capacity, k, kind, gen)
+    out = ref.poisoned((h.capacity, n), torch.bfloat16)
+    h.expert_w4(x, ep.pack_w4(codes, scales), sf=sf, out=out)
+    _check(h, idx, x64, ref.w4_values(codes, scales, group), _scales64(scales, group, fmt), out,
+           False, "splits")

@@ -617,7 +617,7 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
 //   Outputs a wave and waves a group: the widest that fills the card.  Short rows leave a
 //   block little to do between its first and last loads, which more blocks a compute unit
 //   hide: 64 outputs a wave from 32 steps on only (7168 x 2048, 16 steps, groups of 64, 4
-//   rows: 87 with 64, 81 with 32).  Two waves a group below 3072 tiles (16 experts,
+//   rows: 87 with 64, 81 with 32).  Two waves a group below 8 kBlocks tiles (16 experts,
 //   712 x 1152: 7.8, one wave 8.5), four below 768 if each has a few steps (8 experts, 312 x 5888:
 //   14.9, two waves 17.5; 1208 x 1664, 13 steps: 9.1 and 7.9); of two or three steps one wave
 //   takes all (16 experts of 512 x 256: 4.6, four waves 5.5).

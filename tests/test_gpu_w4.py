@@ -347,7 +347,7 @@ FEW = [  # T, K, E, k, n, format, group, x, token rows, all on one expert
     (4, 1, 4, 8064, 16, INT4, 128, "bf16", False, True),
     (4, 1, 4, 8192, 16, INT4, 128, "bf16", False, True),
     (1, 1, 2, 32768, 16, MX, 32, "f32", True, False),
-    (2, 1, 2, 30720, 16, MX, 32, "f32", True, False),
+    (2, 1, 2, 30592, 16, MX, 32, "f32", True, False),
     (2, 1, 2, 32768, 16, MX, 32, "f32", True, True),
     (1, 1, 1, 32640, 24, INT4, 64, "bf16", True, False),
 ]

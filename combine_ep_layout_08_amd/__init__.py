@@ -606,10 +606,11 @@ def add_rmsnorm_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Te
     _rows_of(rstd, "rstd", (T,), torch.float32)
     if grad_residual is not None:
         _rows_of(grad_residual, "grad_residual", z.shape, torch.bfloat16)
+    _here(grad_y, z, weight, rstd, grad_residual, grad_x, grad_weight, workspace)
     if grad_x is not None:
         _rows_of(grad_x, "grad_x", z.shape, torch.bfloat16)
     elif want_grad_x:
-        grad_x = z.new_empty((T, H))
+        grad_x = torch.empty_like(z)
     if grad_weight is not None:
         _rows_of(grad_weight, "grad_weight", (H,), torch.float32)
     elif want_grad_weight:
@@ -623,10 +624,10 @@ def add_rmsnorm_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Te
         else:
             _dev(workspace, "workspace")
             nbytes = workspace.numel() * workspace.element_size()
-    _here(grad_y, z, weight, rstd, grad_residual, grad_x, grad_weight, workspace)
-    _check(ep_add_rmsnorm_backward(_ptr(grad_y), _ptr(z), _ptr(weight), wdt, _ptr(rstd),
-                                   _ptr(grad_residual), T, H, _ptr(grad_x), _ptr(grad_weight),
-                                   _ptr(workspace), nbytes, _stream()), "ep_add_rmsnorm_backward")
+    _check(lib().ep_add_rmsnorm_backward(
+        grad_y.data_ptr(), z.data_ptr(), weight.data_ptr(), wdt, rstd.data_ptr(),
+        _ptr(grad_residual), T, H, _ptr(grad_x), _ptr(grad_weight), _ptr(workspace), nbytes,
+        _stream()), "ep_add_rmsnorm_backward")
     return grad_x, grad_weight
 
 

@@ -421,3 +421,40 @@ def test_tiles_and_splits(T, K, E, k, n, fmt, group, kind):
     h.expert_w4(x, ep.pack_w4(codes, scales), sf=sf, out=out)
     _check(h, idx, x64, ref.w4_values(codes, scales, group), _scales64(scales, group, fmt), out,
            False, "splits")
+
+
+@pytest.mark.parametrize("fmt,group,kind", [(INT4, 128, "bf16"), (INT4, 32, "f32"),
+                                            (MX, 32, "bf16"), (MX, 32, "f32")])
+def test_few_rows_captured(fmt, group, kind):
+    """A decode step of three tokens captured once: new routing (all rows on one expert,
+    empty slots, the same expert twice in a token) and new rows at every replay."""
+    gen = _gen(15)
+    T, K, E, k, n = 3, 4, 16, 1152, 264
+    codes, scales = ref.random_w4(E, n, k, fmt, group, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    w64, s64 = ref.w4_values(codes, scales, group), _scales64(scales, group, fmt)
+    idx = ref.ids(T, K, E, gen, "cuda")
+    x, sf, x64 = _x(T, k, kind, gen)
+    h = ep.Handle(T, K, E, 1)
+    lay = h.bind_layout(idx)
+    lay()
+    out = torch.zeros((h.capacity, n), dtype=torch.bfloat16, device="cuda")
+    call = h.bind_expert_w4(x, packed, sf=sf, token_rows=True, out=out)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lay()
+        call()
+    routes = [ref.ids(T, K, E, gen, "cuda"), torch.full_like(idx, 7), torch.full_like(idx, -1),
+              torch.tensor([[5, 5, -1, 15], [-1, -1, -1, -1], [0, 5, 5, 5]], device="cuda")]
+    for route in routes:
+        idx.copy_(route)
+        q, s, x64 = _x(T, k, kind, gen)
+        x.copy_(q)
+        if sf is not None:
+            sf.copy_(s)
+        out.copy_(ref.poisoned((h.capacity, n), torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(h, idx, x64, w64, s64, out, True, "captured")

@@ -19,11 +19,13 @@
 //   which the accumulators of all tiles start; a group's sum is then
 //   scaled and added to the total.  28 vector instructions a record: the
 //   conversion is what bounds larger batches.
-//   EP_W4_MXFP4: lane l holds channels 32 (l / 16) .. + 31, one scale group, in order.
-//   With x in E4M3 the codes go as they are into
-//   v_mfma_scale_f32_16x16x128_f8f6f4, which applies the group's exponent (its E4M3
-//   operand has channels 64 h + 16 (l / 16) .. + 15 in half h); with x in bf16
-//   v_cvt_scalef32_pk_bf16_fp4 makes bf16 pairs, exactly.
+//   EP_W4_MXFP4: lane l holds channels 32 (l / 16) .. + 31, one scale group, in order;
+//   v_cvt_scalef32_pk_bf16_fp4 makes pairs of bf16, scaled and exact.
+// x in E4M3 is turned into bf16 (exactly) on its way into LDS.  The scaled instruction on 8-
+// and 4-bit codes, v_mfma_scale_f32_16x16x128_f8f6f4, would take E4M3 and E2M1 as they are, but
+// it drops what is small beside the largest products of its 128 channels (2688 - 2688 + 2^-10
+// gives 0; rows whose large products cancel were off by 262 2^-24 of the sum of |x w|, with the
+// bf16 instruction by less than 2 2^-24), which is less than the binary32 sums promised.
 // Scales: [expert][tile][step], in a step [output][group] for EP_W4_INT4 and
 // [group][output] for EP_W4_MXFP4, so a lane's scales of a step are consecutive.
 #include "ep_layer_internal.h"
@@ -179,17 +181,6 @@ __device__ inline void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// 16 outputs x 16 rows x 128 channels of E2M1 weights, scaled by 2^(scale - 127) in
-// each lane's 32 channels, and E4M3 codes of x.
-__device__ inline f32x4 mfma_mx(u32x4 w, uint32_t scale, u32x4 x0, u32x4 x1, f32x4 c) {
-    const i32x8 a = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-    const i32x8 b = {(int)x0.x, (int)x0.y, (int)x0.z, (int)x0.w,
-                     (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, scale, 0, 127);
-}
-
 // What a wave has read of its weights for one step: NT records and their scales.
 template <int FMT, int GROUP, int NT>
 struct Records {
@@ -227,7 +218,7 @@ constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
 //   the lanes' order (16 bytes a lane, no bank conflicts): loads of 16 rows by 64
 //   bytes keep the address units busy for about 35 cycles each, as long as 400
 //   bytes of weights take at the HBM's rate, and with every wave loading its own x a batch of
-//   16 rows an expert took 290 us instead of 165 (64 experts, 4096 x 7168, MXFP4).
+//   16 rows an expert took 125 us more (64 experts, 4096 x 7168, MXFP4; it takes 187).
 //   The weights of the next D - 1 rounds stay in flight across the rounds'
 //   barriers, which order LDS only.
 //   HELD: a pass has `per` rows at most (one to four) and all of their x is brought to LDS
@@ -239,10 +230,9 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
                                                            int per) {
     typedef Records<FMT, GROUP, NT> R;
     constexpr bool MX = FMT == EP_W4_MXFP4;
-    constexpr bool DIRECT = MX && FP8;           // codes go to the matrix instruction as they are
     constexpr int NW = kW4Waves / KS;
     constexpr int P = MX ? 1 : 128 / GROUP;      // groups of a step that are scaled afterwards
-    constexpr int U = DIRECT ? 2 : 4;            // 16-byte units of x a lane, row and step
+    constexpr int U = 4;                         // 16-byte units of x a lane, row and step
     constexpr int F = MT * U;                    // units of x a lane and round
     constexpr int PER = F > NW ? F / NW : 1;     // of them a wave brings
     constexpr int SPER = MT > NW ? MT / NW : 1;  // tiles' scales of x it brings
@@ -322,8 +312,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     if (!HELD)
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        const int i = (p * NW + nw) % F, j = i % U;
-        const int ch = DIRECT ? 64 * j + 16 * q : first_channel(!MX, j, q);
+        const int i = (p * NW + nw) % F, ch = first_channel(!MX, i % U, q);
         xp[p] = static_cast<const char *>(a.x) +
                 (source(i / U) * a.k + held(kg) * 128 + ch) * (FP8 ? 1 : 2);
     }
@@ -341,7 +330,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     auto load_x = [&](X &r, int round) {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            if (FP8 && !DIRECT) {
+            if (FP8) {
                 const u32x2 v = *reinterpret_cast<const u32x2 *>(xp[p]);
                 r.v[p].x = v.x;
                 r.v[p].y = v.y;
@@ -363,7 +352,7 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const uint32_t keep = step(round) < steps ? 0xFFFFFFFFu : 0u;
-            const u32x4 v = FP8 && !DIRECT ? e4m3_bf16(u32x2{r.v[p].x, r.v[p].y}) : r.v[p];
+            const u32x4 v = FP8 ? e4m3_bf16(u32x2{r.v[p].x, r.v[p].y}) : r.v[p];
             lds[(buf * F + (p * NW + nw) % F) * 64 + lane] = v & keep;
         }
         if (FP8) {
@@ -378,9 +367,9 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int u = 0; u < NT; ++u) total[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // HELD: row m's units (16 channels of bf16 or E4M3 a unit of 16 bytes or, converted, 8) start
-    // at m * pitch, an odd number so that rows lie in different banks; behind the rows
-    // the zeros that steps behind the last read, and the scales.
+    // HELD: row m's units (8 channels in 16 bytes) start at m * pitch, an odd number so that rows
+    // lie in different banks; behind the rows the zeros that steps behind the last read, and the
+    // scales.
     constexpr int kStepUnits = 4 * U;
     const int pitch = steps * kStepUnits + 1, zeros = per * pitch;
     float *const held_sf = reinterpret_cast<float *>(all + zeros + kStepUnits);
@@ -388,9 +377,9 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     auto compute = [&](const R &r, int half, int round) {
         const int s = step(round);
         const u32x4 *xl = HELD ? all + (s < steps ? my_row * pitch + s * kStepUnits : zeros) +
-                                     (MX && !FP8 ? 4 * q : q)
+                                     (MX ? 4 * q : q)
                                : lds + (half * KS + kg) * F * 64 + lane;
-        constexpr int kUnit = !HELD ? 64 : MX && !FP8 ? 1 : 4;      // from one unit to the next
+        constexpr int kUnit = !HELD ? 64 : MX ? 1 : 4;      // from one unit to the next
         f32x4 sx[MT];                            // of the rows that a lane has sums of
         if (FP8)
 #pragma unroll
@@ -427,27 +416,18 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
 #pragma unroll
                 for (int u = 0; u < NT; ++u) acc[t][u] = MX && !FP8 ? total[t][u] : from;
             }
-            if (DIRECT) {
 #pragma unroll
-                for (int u = 0; u < NT; ++u)
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                    const uint32_t w4 = r.w[u][(g * J + j) % 4];
+                    const u32x4 w = MX ? mxfp4(w4, r.sw[u][0])
+                                       : int4_plus128(w4, mask, one28);
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
-                        acc[t][u] = mfma_mx(r.w[u], r.sw[u][0], xs[t][0],
-                                            xs[t][1 % J], acc[t][u]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) {
-                        const uint32_t w4 = r.w[u][(g * J + j) % 4];
-                        const u32x4 w = MX ? mxfp4(w4, r.sw[u][0])
-                                           : int4_plus128(w4, mask, one28);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-                            acc[t][u] = MX ? mfma(w, xs[t][j], acc[t][u])
-                                           : mfma(xs[t][j], w, acc[t][u]);
-                    }
-            }
+                        acc[t][u] = MX ? mfma(w, xs[t][j], acc[t][u])
+                                       : mfma(xs[t][j], w, acc[t][u]);
+                }
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
                 const uint32_t sw = r.sw[u][g / 2 % R::kScaleWords];
@@ -478,8 +458,8 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
 #pragma unroll 4
             for (int u = tid; u < steps * kStepUnits; u += kW4Threads)
                 all[m * pitch + u] =
-                    FP8 && !DIRECT ? e4m3_bf16(reinterpret_cast<const u32x2 *>(row)[u])
-                                   : reinterpret_cast<const u32x4 *>(row)[u];
+                    FP8 ? e4m3_bf16(reinterpret_cast<const u32x2 *>(row)[u])
+                        : reinterpret_cast<const u32x4 *>(row)[u];
             if (FP8)
                 for (int s = tid; s < steps; s += kW4Threads)
                     held_sf[m * steps + s] = load_scale(a.sf.p, a.sf.ts, a.sf.hs, from, s,
@@ -578,9 +558,8 @@ hipError_t launch_w4(const W4Args &a, int64_t active, int64_t slots, hipStream_t
 constexpr int kHeldBytes = 64 * 1024;            // two blocks a compute unit
 
 // LDS of a pass of `per` rows held whole, room for the sums of the waves at least.
-int held_bytes(int per, int steps, int tiles_a_wave, bool direct, bool fp8) {
-    const int units = direct ? 8 : 16;
-    const int64_t x = 16 * (per * (int64_t(steps) * units + 1) + units) +
+int held_bytes(int per, int steps, int tiles_a_wave, bool fp8) {
+    const int64_t x = 16 * (per * (int64_t(steps) * 16 + 1) + 16) +
                       (fp8 ? int64_t(4) * per * steps : 0);
     const int sums = 16 * kW4Waves * tiles_a_wave * 64;
     return x > kHeldBytes ? kHeldBytes + 1 : x > sums ? static_cast<int>(x) : sums;
@@ -591,7 +570,7 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
                        hipStream_t stream) {
     return launch_w4<FMT, GROUP, FP8, NT, 1, 4, D, true>(
         a, active, slots, stream, per,
-        held_bytes(per, a.k / 128, NT, FMT == EP_W4_MXFP4 && FP8, FP8));
+        held_bytes(per, a.k / 128, NT, FP8));
 }
 
 // Tile and split, by the sizes that the host knows (us at 64 experts of 4096 x 7168 and
@@ -599,8 +578,9 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
 // the passes that there will be at least; kBlocks is one and a half blocks a compute unit.
 //   Few rows: x is held, in passes of up to four rows, while it takes at most 64 KB.  An expert
 //   with more rows reads its weights again, which is the cost: EP_W4_INT4 153 without and
-//   143 with at 2 rows an expert on average, 183 and 201 at 4; EP_W4_MXFP4 97.4 and 96.5 at
-//   one, 132 and 136 at two (9 tokens, 320 x 4224: 13.4 and 10.8).  Up to four tokens no expert
+//   143 with at 2 rows an expert on average, 183 and 201 at 4; EP_W4_MXFP4 with E4M3 rows 100
+//   and 98 at one, 129 and 127 at one and a half, 141 and 146 at two (9 tokens of 8 experts, 320 x
+//   4224: 10.4 and 9.9).  Up to four tokens no expert
 //   has more (4 tokens, 8 experts of 2192 x 6272, 2.5 rows: 22.5 and 19.2), and in a small grid
 //   more passes fill the card (8 experts of 360 x 1920, 14 rows: 7.8 and 7.1; no longer with
 //   1320 tiles: 312 x 5888, 33 rows, 14.9 and 17.5).  Four waves a group, 64 outputs a wave or,
@@ -609,10 +589,12 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
 //   Otherwise, rows a pass: 16 or 32.  The codes' conversion and the weights' reading are paid
 //   once a pass, an empty half of a wide one costs its matrix instructions.
 //   EP_W4_INT4: 159 (16) and 184 (32) at 8 rows an expert on average, 189 and 189 at 12, 226
-//   and 194 at 16; so 32 beyond 12.  EP_W4_MXFP4 converts nothing: 152 and 152 at 4
-//   rows, 215 and 165 at 16; so 32 beyond 6.  But only where wide passes fill the card too:
+//   and 194 at 16; so 32 beyond 12.  EP_W4_MXFP4 converts less: with E4M3 rows 159 and 179 at 8
+//   rows, 181 and 182 at 10, 225 and 189 at 16, with bf16 rows 159 and 168, 178 and 171, 224 and
+//   181; so 32 beyond 9.  But only where wide passes fill the card too:
 //   EP_W4_INT4 with 2304 tiles (32 experts, 1152 x 2304, 17.6 rows) 23.1 (16) and 25.1;
-//   EP_W4_MXFP4 with 2052 tiles (16 experts, 1824 x 4480, 36 rows) 41.8 and 33.9.  64 rows gave
+//   EP_W4_MXFP4 with 2052 tiles (16 experts, 1824 x 4480, 36 rows) 42.2 and 39.5, with 512 (8
+//   experts, 1024 x 4096, 32 rows) 17.6 and 28.9.  64 rows gave
 //   nothing (16 experts of 64 rows: 150 against 135).
 //   Outputs a wave and waves a group: the widest that fills the card.  Short rows leave a
 //   block little to do between its first and last loads, which more blocks a compute unit
@@ -622,14 +604,13 @@ hipError_t launch_held(const W4Args &a, int64_t active, int64_t slots, int per,
 //   14.9, two waves 17.5; 1208 x 1664, 13 steps: 9.1 and 7.9); of two or three steps one wave
 //   takes all (16 experts of 512 x 256: 4.6, four waves 5.5).
 //   Three steps in registers instead of two keep more of the weights in flight where a
-//   block is short of waves or, EP_W4_MXFP4, a step is long (64 outputs of 32 rows: 173 -> 169
-//   at 16 rows an expert; EP_W4_INT4, which has more to do a step, 194 and 193, with groups
-//   of 32 217 and 228).
+//   block is short of waves.  With 64 outputs of 32 rows they cost waves: 16 rows an expert,
+//   EP_W4_MXFP4 189 with two and 192 with three (25 rows, UE8M0 scales: 222 and 256), EP_W4_INT4
+//   193 and 194, with groups of 32 217 and 228.
 template <int FMT, int GROUP, bool FP8>
 hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     constexpr bool MX = FMT == EP_W4_MXFP4;
     constexpr int64_t kBlocks = 384;
-    constexpr int deep = MX ? 3 : 2;
     const int64_t slots = static_cast<int64_t>(a.num_tokens) * a.num_topk, experts = a.num_experts;
     const int64_t active = slots < experts ? slots : experts;
     const int steps = a.k / 128;
@@ -640,14 +621,14 @@ hipError_t choose_w4(const W4Args &a, hipStream_t stream) {
     const int per = a.num_tokens < 4 ? a.num_tokens : 4;
     const bool few = a.num_tokens <= 4 || 2 * slots <= (MX ? 3 : 4) * experts ||
                      tiles_of(4) <= 2 * kBlocks;
-    if (few && steps >= 4 && held_bytes(per, steps, 4, MX && FP8, FP8) <= kHeldBytes)
+    if (few && steps >= 4 && held_bytes(per, steps, 4, FP8) <= kHeldBytes)
         return tiles_of(per) >= 5 * kBlocks
                    ? launch_held<FMT, GROUP, FP8, 4, 2>(a, active, slots, per, stream)
                    : launch_held<FMT, GROUP, FP8, 2, 3>(a, active, slots, per, stream);
-    const bool wide = slots > (MX ? 6 : 12) * experts && tiles_of(32) >= (MX ? 4 : 8) * kBlocks;
+    const bool wide = slots > (MX ? 9 : 12) * experts && tiles_of(32) >= (MX ? 4 : 8) * kBlocks;
     const int64_t tiles = tiles_of(wide ? 32 : 16);
     if (tiles >= 16 * kBlocks && steps >= 32)
-        return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, deep>(a, active, slots, stream)
+        return wide ? launch_w4<FMT, GROUP, FP8, 4, 2, 1, 2>(a, active, slots, stream)
                     : launch_w4<FMT, GROUP, FP8, 4, 1, 1, 2>(a, active, slots, stream);
     if (wide) return launch_w4<FMT, GROUP, FP8, 2, 2, 1, 2>(a, active, slots, stream);
     if (tiles >= 8 * kBlocks || steps < 4)

@@ -458,3 +458,45 @@ def test_few_rows_captured(fmt, group, kind):
         graph.replay()
         torch.cuda.synchronize()
         _check(h, idx, x64, w64, s64, out, True, "captured")
+
+
+@pytest.mark.parametrize("fmt,group,kind", [(INT4, 32, "bf16"), (INT4, 128, "f32"),
+                                            (MX, 32, "bf16"), (MX, 32, "f32"), (MX, 32, "ue8m0")])
+@pytest.mark.parametrize("T,k", [(1, 128), (1, 640), (3, 896), (20, 128), (20, 640), (40, 640)])
+def test_small_products_beside_large_ones(fmt, group, kind, T, k):
+    """Two large products that cancel and a small one: whatever the order, each partial sum
+    has 24 bits at most (MXFP4: 448 * 6 = 21 * 2^7 and 2^-9 * 0.5, 22 bits; INT4: up to
+    2 * 279 * 28 < 2^14 and multiples of 2^-6, 20 bits), so binary32 sums are exact."""
+    say("w4 small", fmt, group, kind, T, k)
+    n = 40
+    large, small, c_large, c_small, w_small = ((28.0, 2.0 ** -6, 15, 9, 1.0) if fmt == INT4 else
+                                               (448.0, 2.0 ** -9, 7, 1, 0.5))
+    code = torch.full((1, n, k), c_large, dtype=torch.uint8, device="cuda")
+    code[..., ::4] = c_small
+    codes = (code[..., 0::2] | (code[..., 1::2] << 4)).contiguous()
+    if fmt == INT4:
+        scales = torch.ones((1, n, k // group), device="cuda").bfloat16()
+    else:
+        scales = torch.full((1, n, k // group), 127, dtype=torch.uint8, device="cuda")
+    packed = ep.pack_w4(codes, scales)
+    h = ep.Handle(T, 1, 1, 1)
+    h.layout(torch.zeros((T, 1), dtype=torch.int64, device="cuda"))
+    rows = torch.arange(T, device="cuda")
+    for far in (1, 2, 18, 50, 125):                     # places of the three within the row
+        at = (rows * 37 + far * 4) % (k // 4) * 4
+        x = torch.zeros((T, k), device="cuda")
+        x[rows, at] = small
+        x[rows, (at + 1) % k] = large
+        other = (at + 1 + far) % k
+        x[rows, torch.where(other % 4 == 0, (other + 1) % k, other)] = -large
+        if kind == "bf16":
+            q, sf = x.bfloat16(), None
+        else:
+            q = x.to(torch.float8_e4m3fn).view(torch.uint8)
+            sf = (torch.ones((T, k // 128), device="cuda") if kind == "f32" else
+                  torch.full((T, (k // 128 + 3) // 4), 0x7F7F7F7F, dtype=torch.int32,
+                             device="cuda"))
+        assert bool((x.sum(1) == small).all())
+        y = h.expert_w4(q, packed, sf=sf, token_rows=True)
+        assert torch.equal(y.double(), torch.full((T, n), small * w_small, device="cuda",
+                                                  dtype=torch.float64)), far

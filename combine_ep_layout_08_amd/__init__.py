@@ -389,8 +389,9 @@ class BoundCall:
 
     Calling it enqueues the same call on the current stream (read at every
     call) and returns what the direct method returns.  It keeps the tensors it
-    was bound to alive: their contents may change between calls (new routing,
-    new payloads), their storage and shapes may not.  A direct method spends
+    was bound to alive, and the handle whose workspace the call reads: their
+    contents may change between calls (new routing, new payloads), their storage
+    and shapes may not.  A direct method spends
     about 5-6 us of host time per call on validation and marshalling, a bound
     call about 3 us (the C entry point and the launch), which lets small
     batches run at the GPU's pace.
@@ -813,7 +814,7 @@ class Handle:
             col_major_sf, cumulative_stats, streaming)
         self.topk_idx = topk_idx
         # no token-count check: the call lays the batch out itself
-        return BoundCall(fn, args, "ep_layout_dispatch", result, keep)
+        return BoundCall(fn, args, "ep_layout_dispatch", result, (self, keep))
 
     def import_layout(self, topk_idx: torch.Tensor, counts, psum, dst_slot, src_meta,
                       num_recv_tokens: int) -> "Handle":
@@ -876,7 +877,7 @@ class Handle:
         fn, args, result, keep = self._dispatch_call(x, sf, topk_weights, zero_padding, out_x,
                                                       out_sf, out_w, want_weights, col_major_sf,
                                                       streaming=streaming)
-        return BoundCall(fn, args, "ep_dispatch", result, keep, self.h)
+        return BoundCall(fn, args, "ep_dispatch", result, (self, keep), self.h)
 
     def _dispatch_call(self, x, sf, topk_weights, zero_padding, out_x, out_sf, out_w,
                        want_weights, col_major_sf, num_tokens=None, streaming=False):
@@ -969,7 +970,7 @@ class Handle:
         """``combine`` bound to these tensors (see BoundCall); each call
         returns ``out``."""
         fn, args, out, keep = self._combine_call(y, topk_weights, bias, out, bias_0, bias_1)
-        return BoundCall(fn, args, "ep_combine", out, keep, self.h)
+        return BoundCall(fn, args, "ep_combine", out, (self, keep), self.h)
 
     def _combine_call(self, y, topk_weights, bias, out, bias_0, bias_1):
         T = self.h.num_tokens
@@ -1182,7 +1183,7 @@ class Handle:
                        out: Optional[torch.Tensor] = None) -> BoundCall:
         """``expert_w4`` bound to these tensors (see BoundCall)."""
         fn, args, out, keep = self._expert_w4_call(x, weights, sf, token_rows, out)
-        return BoundCall(fn, args, "ep_expert_w4", out, keep, self.h)
+        return BoundCall(fn, args, "ep_expert_w4", out, (self, keep), self.h)
 
     def _expert_w4_call(self, x, weights, sf, token_rows, out):
         rows = self.h.num_tokens if token_rows else self.capacity
@@ -1245,7 +1246,7 @@ class Handle:
         fn, args, result, keep = self._swiglu_call(gate_up, row_weights, scale_format, out,
                                                    out_sf, checkpoint, saved, saved_sf,
                                                    col_major_sf)
-        return BoundCall(fn, args, "ep_swiglu", result, keep, self.h)
+        return BoundCall(fn, args, "ep_swiglu", result, (self, keep), self.h)
 
     def _swiglu_call(self, gate_up, row_weights, scale_format, out, out_sf, checkpoint, saved,
                      saved_sf, col_major_sf):

@@ -3,6 +3,9 @@ C library records every call, host tensors stand in for device tensors, and
 the tests check the argument plumbing - pointers, element strides, scale-pack
 counts, the column-major TMA stride, argument order, the stream, status
 codes turned into exceptions, and that the handle keeps its topk_idx."""
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -186,3 +189,43 @@ def test_bound_call_raises_on_status(fake):
     fake.status = ep.EP_ERR_NOT_LAID_OUT
     with pytest.raises(ep.EpError):
         bc()
+
+
+def _bound(h):
+    """One call of every bind_* method of a handle, by name."""
+    T, K = 16, 4
+    x = torch.zeros((T, 256), dtype=torch.bfloat16)
+    rows = torch.zeros((h.capacity, 256), dtype=torch.bfloat16)
+    idx = torch.zeros((T, K), dtype=torch.int32)
+    weights = ep.W4Weights(torch.zeros(8 * 16 * 128, dtype=torch.uint8),
+                           torch.zeros(8 * 16 * 8, dtype=torch.uint8), 8, 16, 256,
+                           ep.EP_W4_MXFP4, 32)
+    return {"bind_layout": lambda: h.bind_layout(idx),
+            "bind_layout_dispatch": lambda: h.bind_layout_dispatch(idx, x),
+            "bind_dispatch": lambda: h.bind_dispatch(x),
+            "bind_combine": lambda: h.bind_combine(rows),
+            "bind_expert_w4": lambda: h.bind_expert_w4(rows, weights),
+            "bind_swiglu": lambda: h.bind_swiglu(rows)}
+
+
+def test_every_bind_method_is_listed():
+    names = {n for n in dir(ep.Handle) if n.startswith("bind_")}
+    assert names == set(_bound(type("H", (), {"capacity": 1})))
+
+
+@pytest.mark.parametrize("name", ["bind_layout", "bind_layout_dispatch", "bind_dispatch",
+                                  "bind_combine", "bind_expert_w4", "bind_swiglu"])
+def test_bound_calls_keep_the_handles_workspace(fake, name):
+    """The kernels read counts, rows and the error word in the handle's workspace: a bound
+    call that outlives the caller's handle holds it."""
+    h = _handle(fake)
+    workspace = weakref.ref(h.workspace)
+    call = _bound(h)[name]()
+    del h
+    gc.collect()
+    assert workspace() is not None
+    call()
+    assert fake.calls[-1][0] == name.replace("bind", "ep")
+    del call
+    gc.collect()
+    assert workspace() is None

@@ -252,9 +252,11 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     asm("" : "+s"(mask));
     asm("" : "+v"(one28));
 
-    const Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, per,
-                                lane);
+    Pass pass = find_pass(a.counts, a.psum, a.num_experts, first_pass + blockIdx.y, per, lane);
     if (pass.expert < 0 || (bits & EP_ERRBIT_FATAL)) return;
+    // no layout content sends a load or a store out of the rows' buffers
+    if (pass.start < 0 || pass.start >= a.capacity) return;
+    if (pass.rows > a.capacity - pass.start) pass.rows = static_cast<int>(a.capacity - pass.start);
     // The group's records are consecutive; tiles behind the last are read as the
     // last and not stored.
     constexpr int kScaleStep = MX ? 64 : 32 * P;                     // bytes of a record's scales
@@ -303,7 +305,10 @@ __global__ __launch_bounds__(kW4Threads, 2) void w4_kernel(const W4Args a, int f
     const uint32_t *sp[SPER];
     auto row_of = [&](int m) {
         const int64_t row = pass.start + m;
-        return a.token_rows ? static_cast<int64_t>(a.src_meta[row] / a.num_topk) : row;
+        if (!a.token_rows) return row;
+        // a call captured for fewer tokens than a later layout has reads the last of its own
+        const int64_t token = a.src_meta[row] / a.num_topk;
+        return token < 0 ? 0 : token < a.num_tokens ? token : a.num_tokens - 1;
     };
     auto source = [&](int t) {
         const int m = 16 * t + (lane & 15);

@@ -500,3 +500,83 @@ def test_small_products_beside_large_ones(fmt, group, kind, T, k):
         y = h.expert_w4(q, packed, sf=sf, token_rows=True)
         assert torch.equal(y.double(), torch.full((T, n), small * w_small, device="cuda",
                                                   dtype=torch.float64)), far
+
+
+@pytest.mark.parametrize("fmt,group", [(INT4, 64), (MX, 32)])
+@pytest.mark.parametrize("T,k", [(4, 640), (40, 256)])       # rows held whole, and streamed
+def test_layout_content_stays_in_the_buffers(fmt, group, T, k):
+    """Segments and source slots outside the buffers (here written into the handle's
+    workspace) reach no row outside them.  The buffers lie inside larger ones, whose rest
+    must stay untouched and unread."""
+    say("w4 bounds", fmt, group, T, k)
+    gen = _gen(21)
+    n, cap = 40, 2 * T
+    codes, scales = ref.random_w4(2, n, k, fmt, group, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    h = ep.Handle(T, 1, 2, 1, capacity=cap)
+    h.layout(torch.ones((T, 1), dtype=torch.int64, device="cuda"))
+    whole_x = torch.full((3 * cap, k), float("nan"), device="cuda").bfloat16()
+    whole_x[cap:2 * cap] = torch.randn((cap, k), generator=gen, device="cuda").bfloat16()
+    whole = ref.poisoned((3 * cap, n), torch.bfloat16)
+    x, out = whole_x[cap:2 * cap], whole[cap:2 * cap]
+    w64, s64 = ref.w4_values(codes, scales, group)[1], _scales64(scales, group, fmt)
+
+    def close(got, x64, what):
+        want = x64 @ w64.t()
+        size = x64.abs() @ (w64.abs() if s64 is None else s64[1] * 136.0).t()
+        ref.assert_close(got, want, want.abs() * ref.BF16 + size * 66 * ref.F32 + 1e-38, what)
+
+    inside = T // 2
+    h.psum[1] = cap - inside                            # the segment's second half lies behind
+    h.expert_w4(x, packed, out=out)
+    close(out[cap - inside:], x[cap - inside:].double(), "last rows")
+    assert ref.untouched(whole, torch.arange(2 * cap - inside, 2 * cap, device="cuda"))
+    whole.copy_(ref.poisoned(whole.shape, whole.dtype))
+    for start in (-inside, cap):
+        h.psum[1] = start
+        h.expert_w4(x, packed, out=out)                 # what lies inside may be written
+        assert ref.untouched(whole, torch.arange(cap, 2 * cap, device="cuda"))
+
+    h.psum[1] = 0                                       # tokens before and behind the batch
+    h.src_meta[:T] = torch.arange(T, device="cuda", dtype=torch.int32)
+    h.src_meta[1], h.src_meta[2] = -3, T + 1
+    tokens = whole_x[cap:cap + T]
+    whole_x[cap + T:] = float("nan")
+    h.expert_w4(tokens, packed, token_rows=True, out=out)
+    at = torch.arange(T, device="cuda")
+    at[1], at[2] = 0, T - 1
+    close(out[:T], tokens[at].double(), "tokens")
+
+
+def test_a_copied_handle_of_fewer_tokens():
+    """What a captured call sees after a layout of a larger batch: rows of its own tokens
+    are right, and no row behind its batch is read."""
+    gen = _gen(22)
+    T, K, E, k, n = 12, 2, 4, 384, 24
+    codes, scales = ref.random_w4(E, n, k, INT4, 128, gen, "cuda")
+    packed = ep.pack_w4(codes, scales)
+    w64 = ref.w4_values(codes, scales, 128)
+    s64 = _scales64(scales, 128, INT4)
+    h = ep.Handle(2 * T, K, E, 1)
+    few, many = ref.ids(T, K, E, gen, "cuda"), ref.ids(2 * T, K, E, gen, "cuda")
+    h.layout(few)
+    old = ep.ep_handle.from_buffer_copy(h.h)
+    whole = torch.full((2 * T, k), float("nan"), device="cuda").bfloat16()
+    whole[:T] = torch.randn((T, k), generator=gen, device="cuda").bfloat16()
+    out = ref.poisoned((h.capacity, n), torch.bfloat16)
+    h.layout(many)
+    say("w4 copied handle")
+    status = ep.ep_expert_w4(old, whole.data_ptr(), ep.EP_BF16, 1, k, None, 0, 0, 0,
+                             packed.codes.data_ptr(), packed.scales.data_ptr(), INT4, 128, n,
+                             out.data_ptr(), ep._stream())
+    assert status == ep.EP_OK
+    rows, expert, token = ref.rows_of(h, many)
+    written = (out[rows].view(torch.int16) != 0x5A5A).any(1)
+    assert not bool(out[rows][written].isnan().any())
+    mine = written & (token < T)
+    assert bool(mine.any())
+    x64 = whole[token[mine]].double()
+    want = torch.stack([x64[i] @ w64[e].t() for i, e in enumerate(expert[mine].tolist())])
+    size = torch.stack([x64[i].abs() @ (s64[e] * 136.0).t()
+                        for i, e in enumerate(expert[mine].tolist())])
+    ref.assert_close(out[rows[mine]], want, want.abs() * ref.BF16 + size * 66 * ref.F32, "own")

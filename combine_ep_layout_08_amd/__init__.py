@@ -633,10 +633,21 @@ def add_rmsnorm_backward(grad_y: torch.Tensor, z: torch.Tensor, weight: torch.Te
 
 
 class W4Weights:
-    """The experts' 4-bit weights in the layout of ep_expert_w4 (``pack_w4``)."""
+    """The experts' 4-bit weights in the layout of ep_expert_w4: what ``pack_w4``
+    makes, or the same bytes from a file."""
     __slots__ = ("codes", "scales", "num_experts", "n", "k", "format", "group")
 
     def __init__(self, codes, scales, num_experts, n, k, fmt, group):
+        # the kernel reads as many bytes as the sizes say
+        _dev(codes, "codes")
+        _dev(scales, "scales")
+        nc, ns = ep_w4_code_bytes(num_experts, n, k), ep_w4_scale_bytes(num_experts, n, k, fmt,
+                                                                        group)
+        _need(nc > 0 and ns > 0, "invalid sizes of 4-bit weights")
+        _need(codes.numel() * codes.element_size() == nc and
+              scales.numel() * scales.element_size() == ns,
+              f"packed weights of these sizes have {nc} bytes of codes and {ns} of scales")
+        _need(codes.device == scales.device, "codes and scales must be on one device")
         self.codes, self.scales = codes, scales
         self.num_experts, self.n, self.k, self.format, self.group = num_experts, n, k, fmt, group
 

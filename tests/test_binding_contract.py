@@ -4,6 +4,7 @@ the tests check the argument plumbing - pointers, element strides, scale-pack
 counts, the column-major TMA stride, argument order, the stream, status
 codes turned into exceptions, and that the handle keeps its topk_idx."""
 import gc
+import types
 import weakref
 
 import numpy as np
@@ -197,9 +198,9 @@ def _bound(h):
     x = torch.zeros((T, 256), dtype=torch.bfloat16)
     rows = torch.zeros((h.capacity, 256), dtype=torch.bfloat16)
     idx = torch.zeros((T, K), dtype=torch.int32)
-    weights = ep.W4Weights(torch.zeros(8 * 16 * 128, dtype=torch.uint8),
-                           torch.zeros(8 * 16 * 8, dtype=torch.uint8), 8, 16, 256,
-                           ep.EP_W4_MXFP4, 32)
+    weights = types.SimpleNamespace(codes=torch.zeros(8 * 16 * 128, dtype=torch.uint8),
+                                    scales=torch.zeros(8 * 16 * 8, dtype=torch.uint8),
+                                    num_experts=8, n=16, k=256, format=ep.EP_W4_MXFP4, group=32)
     return {"bind_layout": lambda: h.bind_layout(idx),
             "bind_layout_dispatch": lambda: h.bind_layout_dispatch(idx, x),
             "bind_dispatch": lambda: h.bind_dispatch(x),

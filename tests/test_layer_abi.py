@@ -429,3 +429,28 @@ FAR = A16 + (1 << 30)                    # nothing of these sizes reaches from A
 ])
 def test_overlapping_rows_are_refused(call):
     assert call() == ep.EP_ERR_UNSUPPORTED
+
+
+def test_packed_weights_of_other_sizes_are_refused(monkeypatch):
+    """Weights put together by hand: the kernel reads as many bytes as the sizes say, so
+    buffers of any other size are an error and not a read past their end."""
+    monkeypatch.setattr(ep, "_dev", lambda t, name: ep._need(t.is_contiguous(),
+                                                             f"{name} must be contiguous"))
+    E, n, k = 3, 24, 256
+    nc = ep.ep_w4_code_bytes(E, n, k)
+    assert nc == E * 32 * k // 2
+    for fmt, group, ns in ((ep.EP_W4_INT4, 64, E * 32 * 4 * 2), (ep.EP_W4_MXFP4, 32, E * 32 * 8)):
+        assert ep.ep_w4_scale_bytes(E, n, k, fmt, group) == ns
+        codes, scales = (torch.zeros(b, dtype=torch.uint8) for b in (nc, ns))
+        w = ep.W4Weights(codes, scales, E, n, k, fmt, group)
+        assert w.codes is codes and w.scales is scales
+        for bad in ((codes[:-1], scales, E, n, k, fmt, group),
+                    (codes, scales[:-1], E, n, k, fmt, group),
+                    (codes, scales, E + 1, n, k, fmt, group),
+                    (codes, scales, E, n + 16, k, fmt, group),
+                    (codes, scales, E, n, 2 * k, fmt, group),
+                    (codes, scales, E, n, k + 1, fmt, group),
+                    (codes, scales, E, n, k, fmt, 48),
+                    (torch.zeros(2 * nc, dtype=torch.uint8)[::2], scales, E, n, k, fmt, group)):
+            with pytest.raises(ValueError):
+                ep.W4Weights(*bad)

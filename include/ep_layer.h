@@ -129,8 +129,11 @@ ep_status ep_w4_pack(const void *codes, const void *scales, int32_t num_experts,
  *           slot's token, so a decode step needs no dispatch in front of it.
  *   codes, scales  from ep_w4_pack, for the handle's num_experts.
  *   out     device bf16 [capacity, n], 16-byte aligned; combine reads it.
- * The order of the sums depends on the sizes alone.  With EP_W4_INT4 a row
- * that holds an infinity (or whose |x| exceeds 2^120) comes out as NaN.
+ * The order of the sums depends on the sizes alone.  EP_W4_INT4 sums
+ * (128 + code) x - 136 x, partial sums up to 136 times a group's sum of |x|: where
+ * one leaves binary32 (bf16 rows with a group's sum of |x| above 2^120.9) the row's
+ * outputs are infinite, of either sign, or NaN; a row that holds an infinity
+ * comes out as NaN.
  */
 ep_status ep_expert_w4(const ep_handle *h, const void *x, ep_dtype x_dtype, int32_t token_rows,
                        int32_t k, const void *sf, ep_sf_format sf_fmt, int64_t sf_token_stride,

@@ -580,3 +580,28 @@ def test_a_copied_handle_of_fewer_tokens():
     size = torch.stack([x64[i].abs() @ (s64[e] * 136.0).t()
                         for i, e in enumerate(expert[mine].tolist())])
     ref.assert_close(out[rows[mine]], want, want.abs() * ref.BF16 + size * 66 * ref.F32, "own")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,k", [(1, 128), (2, 640), (20, 256), (40, 640)])
+def test_int4_range_of_a_groups_sum(group, T, k):
+    """Partial sums reach 136 times a group's sum of |x|.  With channels of one sign and
+    a sum of 1.75 * 2^120 (238 * 2^120 < 2^128) every product is right; with four times
+    as much the row is infinite or NaN, never a wrong finite number."""
+    say("w4 range", group, T, k)
+    gen = _gen(23)
+    n = 40
+    codes, _ = ref.random_w4(1, n, k, INT4, group, gen, "cuda")
+    scales = torch.full((1, n, k // group), 2.0 ** -20, device="cuda").bfloat16()
+    packed = ep.pack_w4(codes, scales)
+    h = ep.Handle(T, 1, 1, 1)
+    idx = torch.zeros((T, 1), dtype=torch.int64, device="cuda")
+    h.layout(idx)
+    sign = torch.where(torch.arange(T, device="cuda") % 2 == 0, 1.0, -1.0)
+    x = (sign[:, None] * torch.full((T, k), 1.75 * 2.0 ** 120 / group, device="cuda")).bfloat16()
+    y = h.expert_w4(x, packed, token_rows=True)
+    assert bool(torch.isfinite(y).all())
+    _check(h, idx, x.double(), ref.w4_values(codes, scales, group),
+           _scales64(scales, group, INT4), y, True, "range")
+    y = h.expert_w4(x * 4, packed, token_rows=True)
+    assert not bool(torch.isfinite(y).any())

@@ -98,8 +98,9 @@ ep_status ep_add_rmsnorm_backward(const void *grad_y, const void *z, const void 
 typedef enum ep_w4_format {
     EP_W4_INT4 = 0,           /* value (code - 8) * scale, code 0..15, bf16       */
                               /* scales, group 32, 64 or 128                      */
-    EP_W4_MXFP4 = 1           /* E2M1 code * 2^(byte - 127), group 32; byte 255   */
-                              /* makes the group NaN                              */
+    EP_W4_MXFP4 = 1           /* E2M1 code * 2^(byte - 127), group 32: byte 0 is  */
+                              /* 2^-127, a weight of 2^128 or more (bytes 253 and */
+                              /* 254) infinite; byte 255 makes the group NaN      */
 } ep_w4_format;
 
 /*

@@ -605,3 +605,33 @@ def test_int4_range_of_a_groups_sum(group, T, k):
            _scales64(scales, group, INT4), y, True, "range")
     y = h.expert_w4(x * 4, packed, token_rows=True)
     assert not bool(torch.isfinite(y).any())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,k", [(1, 128), (1, 640), (20, 128), (20, 640)])
+@pytest.mark.parametrize("x,code,weight,sf", [(1.0, 0x22, 1.0, 1.0), (2.0 ** -9, 0x11, 0.5, 2.0 ** 20),
+                                              (448.0, 0x77, 6.0, 2.0 ** -20)])
+def test_mxfp4_every_exponent(kind, T, k, x, code, weight, sf):
+    """Every exponent byte in both kinds of rows: byte 0 is 2^-127, products below the
+    normal range are kept, and what leaves binary32 before x's scale is infinite: a product,
+    or a weight (6 * 2^126 and up), which times the row's zeros is NaN."""
+    n = 256
+    codes = torch.full((1, n, k // 2), code, dtype=torch.uint8, device="cuda")
+    e = torch.arange(256, device="cuda").reshape(1, n, 1).expand(1, n, k // 32)
+    h = ep.Handle(T, 1, 1, 1)
+    h.layout(torch.zeros((T, 1), dtype=torch.int32, device="cuda"))
+    say("w4 exponents", kind, T, k, x)
+    row = torch.zeros((T, k), device="cuda")
+    row[torch.arange(T, device="cuda"), (torch.arange(T, device="cuda") * 37 + 40) % k] = x
+    packed = ep.pack_w4(codes, e.to(torch.uint8).contiguous())
+    if kind == "bf16":
+        sf, y = 1.0, h.expert_w4(row.bfloat16(), packed, token_rows=True)
+    else:
+        y = h.expert_w4(row.to(torch.float8_e4m3fn).view(torch.uint8), packed, token_rows=True,
+                        sf=torch.full((T, k // 128), sf, device="cuda"))
+    before = x * weight * torch.exp2(torch.arange(255, device="cuda").double() - 127.0)
+    want = torch.where(before >= 2.0 ** 128, float("inf"), before * sf)
+    want = want.float().bfloat16().double()         # 1, 1/2 and 21 * 2^7 times powers of two
+    fits = int((before / x < 2.0 ** 128).sum())
+    assert torch.equal(y[:, :fits].double(), want[:fits].expand(T, fits))
+    assert fits == (253 if weight == 6.0 else 255) and bool(y[:, fits:].isnan().all())

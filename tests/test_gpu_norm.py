@@ -326,3 +326,52 @@ def test_backward_over_z(T):
     want = ep.add_rmsnorm_backward(g, z, w, rstd)
     got = ep.add_rmsnorm_backward(g, z, w, rstd, grad_x=z)
     assert got[0] is z and torch.equal(z, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_weight_gradient_past_32_bits():
+    """grad_weight over rows on both sides of the first 4 GiB (row 131072).  Of a channel's
+    sum each of the 512 blocks adds up 274 rows in turn, then 4 of its 128 groups and 18 more
+    sums join them, and a term is two rounded products: 298 roundings.  The last rows weigh
+    enough for each of them to show."""
+    T, H, last = 140_000, 16384, 50
+    gen = _gen(31)
+    z = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    g = torch.empty_like(z)
+    rstd = torch.empty(T, device="cuda")
+    w = _weight(H, gen, torch.bfloat16)
+    want = torch.zeros(H, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    say("norm weight gradient offsets", T, H)
+    for a in range(0, T, 4000):
+        z[a:a + 4000] = _rows(4000, H, gen)
+        g[a:a + 4000] = _rows(4000, H, gen, 1e-2)
+        if a + 4000 == T:
+            z[-last:] = torch.where(z[-last:] < 0, -1.0, 1.0)
+            g[-last:] = 1.0
+        rstd[a:a + 4000] = (1.0 / torch.sqrt(z[a:a + 4000].double().square().mean(1) + EPS)).float()
+        term = g[a:a + 4000].double() * z[a:a + 4000].double() * rstd[a:a + 4000].double()[:, None]
+        want += term.sum(0)
+        size += term.abs().sum(0)
+    tol = 298 * ref.F32 * size
+    assert float(tol.max()) < 0.5 * float(term[-last:].abs().min())
+    gx, gw = ep.add_rmsnorm_backward(g, z, w, rstd)
+    ref.assert_close(gw, want, tol, "grad_weight")
+    del gx
+    only = ep.add_rmsnorm_backward(g, z, w, rstd, want_grad_x=False)[1]
+    assert torch.equal(only, gw)
+
+
+@pytest.mark.parametrize("T,H,residual,fmt", [(262_844, 1024, True, "ue8m0"),
+                                              (262_844, 256, False, None)])
+def test_more_rows_than_blocks(T, H, residual, fmt):
+    """More rows than a launch has blocks (2^18): the blocks walk the rest, with the sums of
+    two waves in turn, and with the rows stored past the caches."""
+    test_forward(T, H, residual, torch.bfloat16, fmt)
+
+
+@pytest.mark.parametrize("fmt", [None, "f32", "ue8m0"])
+@pytest.mark.parametrize("T,H", [(13_000, 2048), (4000, 7168), (1700, 16384)])
+def test_rows_stored_past_the_caches(T, H, fmt):
+    """106 to 144 MB of rows, one, two and four vectors a thread: every form of the kernel
+    that stores past the caches."""
+    test_forward(T, H, True, torch.float32, fmt)

@@ -340,3 +340,38 @@ def test_graph():
         rows = ref.rows_of(h, idx)[0]
         for a, b in zip(kept, want):
             assert torch.equal(a[rows].view(torch.uint8), b[rows].view(torch.uint8))
+
+
+def test_more_slots_than_waves():
+    """More slots than the waves of one launch (2^24): the waves walk the rest."""
+    T, inter = (1 << 24) + 1000, 8
+    gen = torch.Generator(device="cuda").manual_seed(41)
+    idx = torch.randint(0, 3, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    h = ep.Handle(T, 1, 3, 1)
+    say("swiglu slots", T, inter)
+    h.layout(idx)
+    assert h.read_counts()["num_expanded"] == T
+    rows = h.dst_slot.reshape(-1).long()
+    gu = torch.randn((T, 2 * inter), generator=gen, device="cuda").bfloat16()
+    w = torch.rand(T, generator=gen, device="cuda")
+    out = ref.poisoned((T, inter), torch.bfloat16)
+    h.swiglu(gu, row_weights=w, out=out)
+    for part in (rows[:1000], rows[(1 << 24) - 1000:]):
+        want, tol = _exact(gu[part], w[part])
+        ref.assert_close(out[part], want, want.abs() * ref.BF16 + tol, "h")
+    g = torch.randn((T, inter), generator=gen, device="cuda").bfloat16()
+    ggu = ref.poisoned((T, 2 * inter), torch.bfloat16)
+    gw = ref.poisoned((T,), torch.float32)
+    again = ref.poisoned((T, inter), torch.bfloat16)
+    h.swiglu_backward(g, gu, row_weights=w, grad_gate_up=ggu, grad_row_weights=gw, out=again)
+    ok = torch.isfinite(gw) & (gw.view(torch.int32) != 0x5A5A5A5A)
+    assert bool(ok.all()) and torch.equal(again.view(torch.int16), out.view(torch.int16))
+    part = rows[(1 << 24) - 1000:]
+    a, b = gu[part].double().chunk(2, 1)
+    s = torch.sigmoid(a)
+    want = torch.cat((b * s * (1.0 + a * (1.0 - s)), a * s), 1) * g[part].double().repeat(1, 2)
+    want *= w[part].double()[:, None]
+    # as in the forward pass; the slope's two terms may cancel, so relative to their sizes
+    size = torch.cat((b.abs() * s * (1.0 + a.abs()), (a * s).abs()), 1) * g[part].double().abs().repeat(1, 2)
+    ref.assert_close(ggu[part], want, want.abs() * ref.BF16 + size * (a.abs().repeat(1, 2) + 8) *
+                     2.0 ** -23, "gradient")

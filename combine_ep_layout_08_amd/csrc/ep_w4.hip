@@ -213,7 +213,7 @@ constexpr uint32_t kNowhere = 0x80000000u;       // behind any view's end
 //   round, four scales a lane and group had to be unpacked and held: groups of 32, 64 outputs
 //   of 32 rows spilled registers; 128 tokens 250 -> 219 us with groups of 32, 4 tokens 78 -> 69.)
 //   EP_W4_MXFP4: the other way round, so a lane has four outputs of one row, one scale of x,
-//   and stores 8 bytes; the weights' scales are the instructions' business.
+//   and stores 8 bytes; the weights' scales are the conversion's business.
 //   x is brought by the block's waves together and handed over through LDS, in
 //   the lanes' order (16 bytes a lane, no bank conflicts): loads of 16 rows by 64
 //   bytes keep the address units busy for about 35 cycles each, as long as 400

@@ -146,6 +146,8 @@ ep_status ep_expert_w4(const ep_handle *h, const void *x, ep_dtype x_dtype, int3
  * Gated activation of the expert rows: with gate = gate_up[r][0 .. inter) and
  * up = gate_up[r][inter .. 2 inter),
  *   h = gate / (1 + exp(-gate)) * up * row_weights[r]
+ * in binary32: for a gate below -87, where exp(-gate) nears the end of its range, the
+ * quotient may come out as 0.
  *   gate_up     device bf16 [capacity, 2 inter], inter % 8 == 0,
  *               inter <= 32768, 16-byte aligned.
  *   row_weights NULL (weight 1) or fp32 [capacity], as dispatch's out_w.

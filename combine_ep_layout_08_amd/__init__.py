@@ -1,8 +1,9 @@
 """MI355X (gfx950) MoE routing layout, dispatch copy and combine, and the
-operators of the expert layer around them (norm, 4-bit products, activation).
+operators of the expert layer around them (norm, activation, the experts'
+products with 4-bit, 8-bit and bf16 weights).
 
-A thin ctypes binding of the C ABI declared in ``include/ep.h`` and
-``include/ep_layer.h`` and built into ``libep.so`` next to this file (``python -m combine_ep_layout_08_amd.build``).
+A thin ctypes binding of the C ABI declared in ``include/ep.h``,
+``include/ep_layer.h`` and ``include/ep_expert.h`` and built into ``libep.so`` next to this file (``python -m combine_ep_layout_08_amd.build``).
 Every step of the computation runs in the library's HIP kernels; this module
 only marshals arguments.  PyTorch supplies device memory and the current
 stream.  There is no fallback: without the built library, every entry point
@@ -35,6 +36,9 @@ __all__ = [
     "ep_add_rmsnorm_backward_workspace", "ep_w4_code_bytes", "ep_w4_scale_bytes", "ep_w4_pack",
     "ep_expert_w4", "ep_swiglu", "ep_swiglu_backward", "add_rmsnorm", "bind_add_rmsnorm",
     "add_rmsnorm_backward", "pack_w4",
+    "ep_quantize_i8", "ep_quantize_i8_rows", "ep_expert_i8", "ep_expert_ffn",
+    "ep_expert_ffn_backward", "ep_expert_ffn_backward_workspace", "quantize_i8",
+    "bind_quantize_i8",
 ]
 
 LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(
@@ -135,6 +139,15 @@ _SIGNATURES = {
                                  _P, ctypes.c_int, _P, _I64, _I64, _P]),
     "ep_swiglu_backward": (ctypes.c_int, [_HP, _P, _I32, _P, _P, ctypes.c_int, ctypes.c_int, _P,
                                           _I64, _I64, _P, _P, _P, _P]),
+    # ep_expert.h
+    "ep_quantize_i8": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P]),
+    "ep_quantize_i8_rows": (ctypes.c_int, [_HP, _P, _I32, _P, _P, _P]),
+    "ep_expert_i8": (ctypes.c_int, [_HP, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _P, _P, _P]),
+    "ep_expert_ffn": (ctypes.c_int, [_HP, _P, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P]),
+    "ep_expert_ffn_backward_workspace": (ctypes.c_size_t, [_HP, _I32]),
+    "ep_expert_ffn_backward": (ctypes.c_int, [_HP, _P, _P, _I32, _I32, _P, _P, _I32, _P, _P, _P,
+                                              _I32, _P, _P, ctypes.c_int, _P, _P, _P, _P,
+                                              ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -330,6 +343,42 @@ def ep_swiglu_backward(h: ep_handle, grad_h_ptr, inter, row_weights_ptr, saved_p
                                     stream)
 
 
+def ep_quantize_i8(x_ptr, num_rows, channels, out_q_ptr, out_scale_ptr, stream) -> int:
+    return lib().ep_quantize_i8(x_ptr, num_rows, channels, out_q_ptr, out_scale_ptr, stream)
+
+
+def ep_quantize_i8_rows(h: ep_handle, x_ptr, channels, out_q_ptr, out_scale_ptr, stream) -> int:
+    return lib().ep_quantize_i8_rows(ctypes.byref(h), x_ptr, channels, out_q_ptr, out_scale_ptr,
+                                     stream)
+
+
+def ep_expert_i8(h: ep_handle, x_ptr, x_scale_ptr, token_rows, k, w_ptr, w_scale_ptr, n, gated,
+                 row_weights_ptr, out_ptr, stream) -> int:
+    return lib().ep_expert_i8(ctypes.byref(h), x_ptr, x_scale_ptr, token_rows, k, w_ptr,
+                              w_scale_ptr, n, gated, row_weights_ptr, out_ptr, stream)
+
+
+def ep_expert_ffn(h: ep_handle, x_ptr, token_rows, hidden, w13_ptr, w2_ptr, inter,
+                  row_weights_ptr, out_h_ptr, saved_ptr, out_y_ptr, stream) -> int:
+    return lib().ep_expert_ffn(ctypes.byref(h), x_ptr, token_rows, hidden, w13_ptr, w2_ptr, inter,
+                               row_weights_ptr, out_h_ptr, saved_ptr, out_y_ptr, stream)
+
+
+def ep_expert_ffn_backward_workspace(h: ep_handle, inter: int) -> int:
+    return int(lib().ep_expert_ffn_backward_workspace(ctypes.byref(h), inter))
+
+
+def ep_expert_ffn_backward(h: ep_handle, grad_y_ptr, x_ptr, token_rows, hidden, w13_ptr, w2_ptr,
+                           inter, row_weights_ptr, saved_ptr, rows_h_ptr, remake_h,
+                           grad_gate_up_ptr, grad_x_ptr, grad_dtype, grad_w13_ptr, grad_w2_ptr,
+                           grad_row_weights_ptr, workspace_ptr, ws_bytes, stream) -> int:
+    return lib().ep_expert_ffn_backward(ctypes.byref(h), grad_y_ptr, x_ptr, token_rows, hidden,
+                                        w13_ptr, w2_ptr, inter, row_weights_ptr, saved_ptr,
+                                        rows_h_ptr, remake_h, grad_gate_up_ptr, grad_x_ptr,
+                                        grad_dtype, grad_w13_ptr, grad_w2_ptr,
+                                        grad_row_weights_ptr, workspace_ptr, ws_bytes, stream)
+
+
 def ep_status_str(status: int) -> str:
     return lib().ep_status_str(status).decode()
 
@@ -489,6 +538,46 @@ def quantize_fp8(x: torch.Tensor, scale_format="f32", out_q=None, out_sf=None,
     _check(ep_quantize_fp8(_ptr(x), T, H, fmt, _ptr(out_q), _ptr(out_sf), ts, hs, _stream()),
            "ep_quantize_fp8")
     return out_q, out_sf
+
+
+def _buffer(t, name, shape, want, device, dtype=torch.bfloat16):
+    """``t``, checked, or a new tensor where none is given and one is wanted."""
+    if t is None and want:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t is not None:
+        _rows_of(t, name, shape, dtype)
+    return t
+
+
+def _i8_rows(x, rows, what, out_q, out_scale):
+    """Check bf16 rows and the buffers of their int8 codes and scales, or make these."""
+    _dev(x, "x")
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and (rows is None or x.shape[0] == rows),
+          f"x must be bf16 [{what}, C]")
+    out_q = _buffer(out_q, "out_q", tuple(x.shape), True, x.device, torch.int8)
+    out_scale = _buffer(out_scale, "out_scale", (x.shape[0],), True, x.device, torch.float32)
+    return out_q, out_scale
+
+
+def _quantize_i8_call(x, out_q, out_scale):
+    out_q, out_scale = _i8_rows(x, None, "T", out_q, out_scale)
+    _here(x, out_q, out_scale)
+    args = (_ptr(x), x.shape[0], x.shape[1], _ptr(out_q), _ptr(out_scale))
+    return lib().ep_quantize_i8, args, (out_q, out_scale), x
+
+
+def quantize_i8(x: torch.Tensor, out_q=None, out_scale=None):
+    """bf16 [T, C] -> (int8 codes [T, C], fp32 scales [T]): scale = max |row| / 127, codes
+    rounded to nearest even.  A row with a NaN or an infinity gets scale NaN and codes 0."""
+    fn, args, result, _ = _quantize_i8_call(x, out_q, out_scale)
+    _check(fn(*args, _stream()), "ep_quantize_i8")
+    return result
+
+
+def bind_quantize_i8(x: torch.Tensor, out_q=None, out_scale=None) -> "BoundCall":
+    """``quantize_i8`` bound to these tensors (see BoundCall)."""
+    fn, args, result, keep = _quantize_i8_call(x, out_q, out_scale)
+    return BoundCall(fn, args, "ep_quantize_i8", result, keep)
 
 
 _CODE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
@@ -1352,3 +1441,168 @@ class Handle:
                                   _ptr(grad_gate_up), _ptr(grad_row_weights), _ptr(out),
                                   _stream()), "ep_swiglu_backward")
         return grad_gate_up, grad_row_weights, out
+
+    def quantize_i8(self, x: torch.Tensor, out_q=None, out_scale=None):
+        """Expert rows bf16 [capacity, C] as int8 codes [capacity, C] with one fp32 scale a
+        row, [capacity] (see ``ep.quantize_i8``).  Rows without a slot are left as they were."""
+        fn, args, result, _ = self._quantize_i8_call(x, out_q, out_scale)
+        _check(fn(*args, _stream()), "ep_quantize_i8_rows")
+        return result
+
+    def bind_quantize_i8(self, x: torch.Tensor, out_q=None, out_scale=None) -> BoundCall:
+        """``quantize_i8`` bound to these tensors (see BoundCall)."""
+        fn, args, result, keep = self._quantize_i8_call(x, out_q, out_scale)
+        return BoundCall(fn, args, "ep_quantize_i8_rows", result, (self, keep), self.h)
+
+    def _quantize_i8_call(self, x, out_q, out_scale):
+        out_q, out_scale = _i8_rows(x, self.capacity, "capacity", out_q, out_scale)
+        _here(x, out_q, out_scale, self.workspace)
+        args = (ctypes.byref(self.h), _ptr(x), x.shape[1], _ptr(out_q), _ptr(out_scale))
+        return lib().ep_quantize_i8_rows, args, (out_q, out_scale), x
+
+    def expert_i8(self, x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor,
+                  w_scale: torch.Tensor, gated: bool = False,
+                  row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Every expert's int8 rows times its int8 weights w [E, n, k], with a scale for each
+        row, x_scale fp32 [rows], and each output channel, w_scale fp32 [E, n]: bf16
+        [capacity, n].  With ``gated`` w is gate above up, and silu(gate) * up
+        (* row_weights) comes out, bf16 [capacity, n/2].  x: [capacity, k] as dispatch
+        writes it, or with ``token_rows`` the tokens' own rows [T, k].  Rows without a
+        slot are left as they were."""
+        fn, args, out, _ = self._expert_i8_call(x, x_scale, w, w_scale, gated, row_weights,
+                                                token_rows, out)
+        _check(fn(*args, _stream()), "ep_expert_i8")
+        return out
+
+    def bind_expert_i8(self, x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor,
+                       w_scale: torch.Tensor, gated: bool = False,
+                       row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                       out: Optional[torch.Tensor] = None) -> BoundCall:
+        """``expert_i8`` bound to these tensors (see BoundCall)."""
+        fn, args, out, keep = self._expert_i8_call(x, x_scale, w, w_scale, gated, row_weights,
+                                                   token_rows, out)
+        return BoundCall(fn, args, "ep_expert_i8", out, (self, keep), self.h)
+
+    def _expert_i8_call(self, x, x_scale, w, w_scale, gated, row_weights, token_rows, out):
+        E, rows = self.h.num_experts, self.h.num_tokens if token_rows else self.capacity
+        _dev(w, "w")
+        _need(w.dtype == torch.int8 and w.dim() == 3 and w.shape[0] == E,
+              f"w must be int8 [{E}, n, k]")
+        n, k = w.shape[1:]
+        _rows_of(x, "x", (rows, k), torch.int8)
+        _rows_of(x_scale, "x_scale", (rows,), torch.float32)
+        _rows_of(w_scale, "w_scale", (E, n), torch.float32)
+        _need(not gated or n % 2 == 0, "gated weights are gate above up")
+        _need(gated or row_weights is None, "row_weights are for gated products")
+        self._row_weights(row_weights)
+        cols = n // 2 if gated else n
+        if out is None:
+            out = torch.empty((self.capacity, cols), dtype=torch.bfloat16, device=x.device)
+        _rows_of(out, "out", (self.capacity, cols), torch.bfloat16)
+        _here(x, x_scale, w, w_scale, row_weights, out, self.workspace)
+        args = (ctypes.byref(self.h), _ptr(x), _ptr(x_scale), 1 if token_rows else 0, k, _ptr(w),
+                _ptr(w_scale), n, 1 if gated else 0, _ptr(row_weights), _ptr(out))
+        return lib().ep_expert_i8, args, out, (x, x_scale, w, w_scale, row_weights)
+
+    def expert_ffn(self, x: torch.Tensor, w13: torch.Tensor, w2: Optional[torch.Tensor],
+                   row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                   want_saved: bool = False, out_h=None, saved=None, out=None):
+        """The experts' gated feed-forward block in bf16: gate and up = w13[e] . x (w13
+        [E, 2 inter, H], gate above up), h = silu(gate) * up (* row_weights), y = w2[e] . h
+        (w2 [E, H, inter]).  x: [capacity, H] as dispatch writes it, or with ``token_rows`` the
+        tokens' own rows [T, H].  Returns (y [capacity, H], h [capacity, inter], saved): with
+        ``want_saved`` gate and up [capacity, 2 inter] for ``expert_ffn_backward``.  With w2
+        None y is None.  Rows without a slot are left as they were."""
+        fn, args, result, _ = self._expert_ffn_call(x, w13, w2, row_weights, token_rows,
+                                                    want_saved, out_h, saved, out)
+        _check(fn(*args, _stream()), "ep_expert_ffn")
+        return result
+
+    def bind_expert_ffn(self, x: torch.Tensor, w13: torch.Tensor, w2: Optional[torch.Tensor],
+                        row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                        want_saved: bool = False, out_h=None, saved=None, out=None) -> BoundCall:
+        """``expert_ffn`` bound to these tensors (see BoundCall)."""
+        fn, args, result, keep = self._expert_ffn_call(x, w13, w2, row_weights, token_rows,
+                                                       want_saved, out_h, saved, out)
+        return BoundCall(fn, args, "ep_expert_ffn", result, (self, keep), self.h)
+
+    def _ffn_sizes(self, w13, w2):
+        E = self.h.num_experts
+        _dev(w13, "w13")
+        _need(w13.dtype == torch.bfloat16 and w13.dim() == 3 and w13.shape[0] == E and
+              w13.shape[1] % 2 == 0, f"w13 must be bf16 [{E}, 2 inter, H]")
+        inter, H = w13.shape[1] // 2, w13.shape[2]
+        if w2 is not None:
+            _rows_of(w2, "w2", (E, H, inter), torch.bfloat16)
+        return H, inter
+
+    def _expert_ffn_call(self, x, w13, w2, row_weights, token_rows, want_saved, out_h, saved, out):
+        cap, dev = self.capacity, x.device
+        H, inter = self._ffn_sizes(w13, w2)
+        _rows_of(x, "x", (self.h.num_tokens if token_rows else cap, H), torch.bfloat16)
+        self._row_weights(row_weights)
+        _need(w2 is not None or out is None, "out needs w2")
+        out_h = _buffer(out_h, "out_h", (cap, inter), True, dev)
+        saved = _buffer(saved, "saved", (cap, 2 * inter), want_saved, dev)
+        out = _buffer(out, "out", (cap, H), w2 is not None, dev)
+        _here(x, w13, w2, row_weights, out_h, saved, out, self.workspace)
+        args = (ctypes.byref(self.h), _ptr(x), 1 if token_rows else 0, H, _ptr(w13), _ptr(w2),
+                inter, _ptr(row_weights), _ptr(out_h), _ptr(saved), _ptr(out))
+        return lib().ep_expert_ffn, args, (out, out_h, saved), (x, w13, w2, row_weights)
+
+    def expert_ffn_backward(self, grad_y: torch.Tensor, x: Optional[torch.Tensor],
+                            w13: torch.Tensor, w2: torch.Tensor, saved: torch.Tensor,
+                            h: Optional[torch.Tensor] = None,
+                            row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                            remake_h: bool = False, grad_gate_up=None, grad_x=None,
+                            want_grad_x: bool = True, grad_w13=None, grad_w2=None,
+                            want_grad_w: bool = True, grad_dtype: torch.dtype = torch.bfloat16,
+                            grad_row_weights=None, want_grad_weights: bool = False,
+                            workspace=None):
+        """Gradients of ``expert_ffn`` from its ``saved`` gate and up and its ``h`` (which
+        ``remake_h`` makes again from ``saved``, into ``h`` if that is given).  Returns (grad_x
+        bf16 [capacity, H] for ``dispatch_backward``, grad_w13, grad_w2 in ``grad_dtype``, bf16 or
+        fp32 (or that of the tensors given), grad_row_weights fp32 [capacity] with
+        ``want_grad_weights``, grad_gate_up bf16 [capacity, 2 inter], which may be ``saved``
+        itself); what is not wanted is None.  Rows without a slot are left as they were."""
+        cap, dev = self.capacity, grad_y.device
+        _need(w2 is not None, "the gradients need w2")
+        H, inter = self._ffn_sizes(w13, w2)
+        _rows_of(grad_y, "grad_y", (cap, H), torch.bfloat16)
+        _rows_of(saved, "saved", (cap, 2 * inter), torch.bfloat16)
+        self._row_weights(row_weights)
+        given = [g.dtype for g in (grad_w13, grad_w2) if g is not None]
+        if given:
+            grad_dtype = given[0]
+        _need(grad_dtype in (torch.bfloat16, torch.float32), "weight gradients are bf16 or fp32")
+        grad_w13 = _buffer(grad_w13, "grad_w13", tuple(w13.shape), want_grad_w, dev, grad_dtype)
+        grad_w2 = _buffer(grad_w2, "grad_w2", tuple(w2.shape), want_grad_w, dev, grad_dtype)
+        grad_x = _buffer(grad_x, "grad_x", (cap, H), want_grad_x, dev)
+        grad_gate_up = _buffer(grad_gate_up, "grad_gate_up", (cap, 2 * inter), True, dev)
+        grad_row_weights = _buffer(grad_row_weights, "grad_row_weights", (cap,),
+                                   want_grad_weights, dev, torch.float32)
+        h = _buffer(h, "h", (cap, inter), remake_h, dev)
+        _need(h is not None or grad_w2 is None, "the gradient of w2 needs h")
+        if x is not None:
+            _rows_of(x, "x", (self.h.num_tokens if token_rows else cap, H), torch.bfloat16)
+        _need(x is not None or grad_w13 is None, "the gradient of w13 needs x")
+        nbytes = 0
+        if grad_row_weights is not None:
+            nbytes = ep_expert_ffn_backward_workspace(self.h, inter)
+            if workspace is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            _dev(workspace, "workspace")
+            _need(workspace.numel() * workspace.element_size() >= nbytes,
+                  f"workspace must have {nbytes} bytes")
+        else:
+            workspace = None
+        _here(grad_y, x, w13, w2, saved, h, row_weights, grad_gate_up, grad_x, grad_w13, grad_w2,
+              grad_row_weights, workspace, self.workspace)
+        _check(ep_expert_ffn_backward(
+            self.h, _ptr(grad_y), _ptr(x), 1 if token_rows else 0, H, _ptr(w13), _ptr(w2), inter,
+            _ptr(row_weights), _ptr(saved), _ptr(h), 1 if remake_h else 0, _ptr(grad_gate_up),
+            _ptr(grad_x), EP_F32 if grad_dtype == torch.float32 else EP_BF16, _ptr(grad_w13),
+            _ptr(grad_w2), _ptr(grad_row_weights), _ptr(workspace), nbytes, _stream()),
+            "ep_expert_ffn_backward")
+        return grad_x, grad_w13, grad_w2, grad_row_weights, grad_gate_up

@@ -1,0 +1,303 @@
+// Matrix product of one block's tile on gfx950, for the experts' products.
+//
+// A tile of the output is BQ rows by BP columns: out[q, p] = sum_c Q(q, c) P(p, c), c the
+// channels that are summed.  P gives the outputs' contiguous dimension.  In memory an operand
+// lies either in rows of channels ("rows": x, or W times x) or channel by channel ("cols":
+// W^T times a gradient, or both operands of a weight gradient, where the channels are the
+// expert's rows).  A chunk is 128 bytes of channels: 64 in bf16, 128 in int8.
+//
+// Chunks go from memory straight to LDS (global_load_lds, 16 bytes a lane), `S` of them in a
+// ring.  Rows operands: an LDS row is 128 bytes, its 16-byte units permuted by u ^ (row % 8), so
+// that the 16 rows a matrix instruction reads are in different banks.  Cols operands: an LDS
+// row is one channel's BQ or BP values; ds_read_b64_tr_b16 hands each lane the four channels of
+// its own column.  The permutations are made by the addresses that the lanes load from, as the
+// load's place in LDS is fixed by the lane.
+#pragma once
+
+#include "ep_layer_internal.h"
+#include "ep_rows.h"
+
+namespace ep {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+#define EP_LDS __attribute__((address_space(3)))
+
+// 16 x 16 outputs of 64 bytes of channels: lane l holds p = l % 16 of the first operand, q =
+// l % 16 of the second, the 16 bytes of channels at 16 (l / 16) of both, and the outputs
+// p = 4 (l / 16) + i of q = l % 16.
+struct Bf16 {
+    typedef f32x4 Acc;
+    static constexpr int kBytes = 2;
+    static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p),
+                                                       __builtin_bit_cast(bf16x8, q), c, 0, 0, 0);
+    }
+};
+
+// Sums of 32768 products of codes stay below 2^30: nothing is rounded.
+struct Int8 {
+    typedef i32x4 Acc;
+    static constexpr int kBytes = 1;
+    static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, p),
+                                                     __builtin_bit_cast(i32x4, q), c, 0, 0, 0);
+    }
+};
+
+// 16 bytes a lane from memory to LDS at `to` + 16 lane, `to` the same in all lanes.  The
+// compiler does not count these loads: wait_loads() does.  (Its builtin makes it wait for all
+// of them before any read of LDS.)  Lanes that are switched off write nothing.
+__device__ inline void load_lds(uint32_t to, const char *base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(to), "v"(off), "s"(base) : "memory");
+}
+
+__device__ inline void load_lds(uint32_t to, const char *from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(to), "v"(from) : "memory");
+}
+
+// Until at most N of the wave's loads are under way, and its LDS stores are done.
+template <int N>
+__device__ inline void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
+}
+
+__device__ inline void block_barrier() {
+    asm volatile("s_barrier" ::: "memory");
+}
+
+__device__ inline uint32_t lds_address(const void *p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((EP_LDS const char *)p));
+}
+
+__device__ inline u32x4 read_lds(uint32_t at) {
+    return *reinterpret_cast<EP_LDS u32x4 *>(static_cast<uintptr_t>(at));
+}
+
+__device__ inline void zero_lds(uint32_t at) {
+    *reinterpret_cast<EP_LDS u32x4 *>(static_cast<uintptr_t>(at)) = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Where the rows of a token-rows call lie: the slot's token, inside the batch whatever the
+// layout holds (a call captured for fewer tokens than a later layout has reads the last of
+// its own).
+__device__ inline int64_t token_of(const int32_t *src_meta, int64_t row, int topk, int tokens) {
+    const int64_t t = src_meta[row] / topk;
+    return t < 0 ? 0 : t < tokens ? t : tokens - 1;
+}
+
+// ---------------------------------------------------------------- operands
+// An operand of R rows in rows of channels.  `Threads` threads bring a chunk in kLoads loads
+// each: load i takes row i * Threads / 8 + thread / 8.  `row_of(i)` gives the row's byte offset
+// from `base` (GATHER: its address).
+template <int R, int Threads, bool GATHER>
+struct RowsOperand {
+    static constexpr int kBytes = R * 128;
+    static constexpr int kLoads = kBytes / (Threads * 16) > 0 ? kBytes / (Threads * 16) : 1;
+    static constexpr bool kPart = kBytes < Threads * 16;     // not every wave loads
+    static_assert(kBytes % (Threads * 16) == 0 || kPart, "whole loads");
+    const char *base;
+    uint32_t off[GATHER ? 1 : kLoads];
+    const char *from[GATHER ? kLoads : 1];
+    uint32_t to;             // of the wave's first load in a stage
+    int unit;                // of 16 bytes in the chunk, the same in every load
+    bool mine;
+
+    static __device__ int row(int i) { return i * (Threads / 8) + threadIdx.x / 8; }
+
+    template <typename RowOf>
+    __device__ void init(const void *b, RowOf row_of) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        base = static_cast<const char *>(b);
+        unit = (threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7);
+        to = wave * 1024;
+        mine = !kPart || wave * 1024 < kBytes;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int64_t at = row_of(mine ? row(i) : 0) + unit * 16;
+            if (GATHER) from[i] = base + at;
+            else off[i] = static_cast<uint32_t>(at);
+        }
+    }
+    // The next chunk to `stage`, of which T has `channels`; what is missing is zeros.
+    template <typename T>
+    __device__ void load(uint32_t stage, int channels) {
+        if (kPart && !mine) return;
+        const bool in = unit * 16 < channels * T::kBytes;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = stage + to + i * Threads * 16;
+            if (in) {
+                if (GATHER) load_lds(at, from[i]);
+                else load_lds(at, base, off[i]);
+            } else {
+                zero_lds(at + (threadIdx.x & 63) * 16);
+            }
+            if (GATHER) from[i] += 128;
+        }
+        if (!GATHER) base += 128;
+    }
+    // The wave's operand of a matrix instruction: rows 16 t .., channels of 64 bytes `half`.
+    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
+        const int lane = threadIdx.x & 63;
+        return read_lds(stage + (16 * t + (lane & 15)) * 128 +
+                        (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4));
+    }
+};
+
+// An operand of C columns, channel by channel, in bf16.  `from(i)` gives the byte offset of the
+// thread's 16 bytes in load i from `base`, or its address (GATHER).
+template <int C, int Threads, bool GATHER>
+struct ColsOperand {
+    static constexpr int kRow = 2 * C;                       // bytes of a channel
+    static constexpr int kBytes = 64 * kRow;
+    static constexpr int kLoads = kBytes / (Threads * 16);
+    static constexpr bool kPart = false, mine = true;
+    static_assert(kBytes % (Threads * 16) == 0 && C >= 128, "whole loads");
+    const char *base;
+    int64_t pitch;           // bytes from a channel to the next
+    uint32_t col;            // byte offset of the thread's unit in its channel, as loaded
+    uint32_t off[kLoads];
+    const int32_t *src_meta; // GATHER: of the segment's rows
+    int topk, tokens;
+    uint32_t to;
+
+    static __device__ int channel(int i) { return (i * Threads + threadIdx.x) / (kRow / 16); }
+    // Units of 32 bytes are permuted by these bits of the channel: a read takes 32 bytes of
+    // four consecutive channels in each row of 16 lanes, rows of lanes being 8 channels apart.
+    static __device__ int swizzle(int ch) { return (ch & 3) | ((ch >> 1) & 4); }
+
+    // Columns `first` .. of `cols` (in a row of `pitch` bytes) from channel 0 at `b`.
+    __device__ void init(const void *b, int64_t row_pitch, int first, int cols) {
+        base = static_cast<const char *>(b);
+        pitch = row_pitch;
+        to = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int ch = channel(i);
+            const int unit = (threadIdx.x % (kRow / 16)) ^ (swizzle(ch) << 1);
+            int c = first + unit * 8;
+            if (c >= cols) c = cols - 8;                     // computed on, and not stored
+            off[i] = (GATHER ? 0u : static_cast<uint32_t>(ch * pitch)) + 2u * c;
+        }
+    }
+    __device__ void gather(const int32_t *meta, int k, int t) {
+        src_meta = meta;
+        topk = k;
+        tokens = t;
+    }
+    // The next chunk to `stage`, of which `channels` are there; what is missing is zeros.
+    template <typename T>
+    __device__ void load(uint32_t stage, int channels) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = stage + to + i * Threads * 16;
+            const int ch = channel(i);
+            if (ch < channels) {
+                if (GATHER)
+                    load_lds(at, base + token_of(src_meta, ch, topk, tokens) * pitch + off[i]);
+                else
+                    load_lds(at, base, off[i]);
+            } else {
+                zero_lds(at + (threadIdx.x & 63) * 16);
+            }
+        }
+        if (GATHER) src_meta += 64;
+        else base += 64 * pitch;
+    }
+    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
+        const int lane = threadIdx.x & 63, j = lane & 15;
+        const int ch = half * 32 + (lane >> 4) * 8 + (j >> 2);
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = ch + 4 * i;
+            const uint32_t at = stage + c * kRow + ((t ^ swizzle(c)) << 5) + (j & 3) * 8;
+            const u32x2 r = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                           reinterpret_cast<EP_LDS s16x4 *>(static_cast<uintptr_t>(at))));
+            v[2 * i] = r.x;
+            v[2 * i + 1] = r.y;
+        }
+        return v;
+    }
+};
+
+// ---------------------------------------------------------------- main loop
+// WQ x WP waves, each TQ x TP tiles of 16 x 16; S chunks in the ring.
+template <typename T, int BQ_, int BP_, int WQ_, int WP_, int S_>
+struct Tile {
+    typedef T Type;
+    static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, S = S_;
+    static constexpr int TQ = BQ / 16 / WQ, TP = BP / 16 / WP;
+    static constexpr int kThreads = 64 * WQ * WP;
+    static constexpr int kBlocks = kThreads >= 512 ? 1 : 512 / kThreads;   // a compute unit: 256 registers
+    typedef typename T::Acc Acc;
+    struct Sums {
+        Acc v[TQ][TP];
+    };
+    static constexpr int kStage = (BQ + BP) * 128;
+    static constexpr int kLds = kStage * S;
+};
+
+// Sums of the tile over `channels` channels.  `lds`: kLds bytes; when this returns a wave may
+// still be reading them.
+template <typename C, typename Q, typename P>
+__device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
+                                    typename C::Sums &sums) {
+    constexpr int S = C::S, kPerChunk = 128 / C::Type::kBytes;
+    constexpr int kLoads = Q::kLoads + P::kLoads;
+    static_assert(!P::kPart, "every wave loads of P");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wq = wave / C::WP, wp = wave % C::WP;
+    const int chunks = (channels + kPerChunk - 1) / kPerChunk;
+#pragma unroll
+    for (int a = 0; a < C::TQ; ++a)
+#pragma unroll
+        for (int b = 0; b < C::TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
+    auto load = [&](int chunk, uint32_t stage) {
+        const int left = channels - chunk * kPerChunk;
+        q.template load<typename C::Type>(stage, left);
+        p.template load<typename C::Type>(stage + C::BQ * 128, left);
+    };
+    uint32_t head = lds, tail = lds;         // stages to load next, to compute on next
+    auto next = [&](uint32_t s) { return s + C::kStage == lds + C::kLds ? lds : s + C::kStage; };
+#pragma unroll
+    for (int i = 0; i + 1 < S; ++i)
+        if (i < chunks) {
+            load(i, head);
+            head = next(head);
+        }
+    for (int c = 0; c < chunks; ++c) {
+        // this chunk has come: at most the S - 2 behind it are still on their way, whole ones
+        if (c + S - 1 >= chunks) wait_loads<0>();
+        else if (Q::kPart && !q.mine) wait_loads<(S - 2) * P::kLoads>();
+        else wait_loads<(S - 2) * kLoads>();
+        block_barrier();
+        if (c + S - 1 < chunks) {
+            load(c + S - 1, head);
+            head = next(head);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            u32x4 fq[C::TQ], fp[C::TP];
+#pragma unroll
+            for (int b = 0; b < C::TP; ++b)
+                fp[b] = P::fragment(tail + C::BQ * 128, wp * C::TP + b, half);
+#pragma unroll
+            for (int a = 0; a < C::TQ; ++a) fq[a] = Q::fragment(tail, wq * C::TQ + a, half);
+#pragma unroll
+            for (int a = 0; a < C::TQ; ++a)
+#pragma unroll
+                for (int b = 0; b < C::TP; ++b)
+                    sums.v[a][b] = C::Type::mma(fp[b], fq[a], sums.v[a][b]);
+        }
+        tail = next(tail);
+    }
+}
+
+}  // namespace ep

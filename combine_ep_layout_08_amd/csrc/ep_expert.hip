@@ -12,8 +12,8 @@ __device__ inline float sigmoid(float g) {
 }
 
 // ---------------------------------------------------------------- tiles of the experts' rows
-// Every expert's rows are cut into row tiles of `per`, and every row tile meets `across`
-// tiles of outputs.
+// Every expert's rows are cut into as few row tiles of at most `per` rows as they need, about
+// equal ones, and every row tile meets `across` tiles of outputs.
 struct Place {
     int expert;              // -1: no such tile
     int start, rows;         // rows of the layout
@@ -62,8 +62,9 @@ __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int 
         const int count = __builtin_amdgcn_readlane(c, l);
         before += __builtin_amdgcn_readlane(upto, l) - tiles;
         const int at = static_cast<int>(tile - before * across);
-        const int first = at % tiles * per;
-        return {e0 + l, seg.psum[e0 + l] + first, count - first < per ? count - first : per,
+        const int size = ((count + tiles - 1) / tiles + 15) / 16 * 16;
+        const int first = at % tiles * size;
+        return {e0 + l, seg.psum[e0 + l] + first, count - first < size ? count - first : size,
                 at / tiles};
     }
     return {-1, 0, 0, 0};
@@ -75,10 +76,29 @@ __device__ inline bool block_tile(const Segments &seg, int64_t first, int per, i
     const uint32_t bits = static_cast<uint32_t>(seg.scalars[EP_SCALAR_ERROR_BITS]);
     *p = find_tile(seg, first + blockIdx.x, per, across, threadIdx.x & 63);
     if (p->expert < 0 || (bits & EP_ERRBIT_FATAL)) return false;
+    // the same in every lane, which the compiler cannot see
+    p->expert = __builtin_amdgcn_readfirstlane(p->expert);
     p->start = __builtin_amdgcn_readfirstlane(p->start);
+    p->rows = __builtin_amdgcn_readfirstlane(p->rows);
+    p->column = __builtin_amdgcn_readfirstlane(p->column);
     if (p->start < 0 || p->start >= seg.capacity) return false;
     if (p->rows > seg.capacity - p->start) p->rows = static_cast<int>(seg.capacity - p->start);
     return true;
+}
+
+// The tile's sums, without the row tiles that it has no rows for.
+template <typename C, typename Q, typename P>
+__device__ inline void expert_product(Q &q, P &p, int channels, int rows, uint32_t lds,
+                                      typename C::Sums &sums) {
+    if constexpr (C::TQ == 8) {
+        const int tiles = (rows + 16 * C::WQ - 1) / (16 * C::WQ);
+        if (tiles > 6) tile_product<C, 8>(q, p, channels, lds, sums);
+        else if (tiles > 4) tile_product<C, 6>(q, p, channels, lds, sums);
+        else if (tiles > 2) tile_product<C, 4>(q, p, channels, lds, sums);
+        else tile_product<C, 2>(q, p, channels, lds, sums);
+    } else {
+        tile_product<C, C::TQ>(q, p, channels, lds, sums);
+    }
 }
 
 enum Out { kPlain, kGated, kGateGrad };
@@ -124,7 +144,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
         const char *w = static_cast<const char *>(a.w) +
                         at.expert * static_cast<int64_t>(a.k) * a.n * 2;
         p.init(w, 2 * static_cast<int64_t>(a.n), p0, a.n);
-        tile_product<C>(q, p, a.k, lds, sums);
+        expert_product<C>(q, p, a.k, at.rows, lds, sums);
     } else {
         RowsOperand<C::BP, C::kThreads, false> p;
         const char *w = static_cast<const char *>(a.w) + at.expert * w_rows * pitch;
@@ -137,14 +157,14 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
             j = j < a.n ? j : a.n - 1;                       // computed on, and not stored
             return (j + (t < G ? 0 : a.n)) * pitch;
         });
-        tile_product<C>(q, p, a.k, lds, sums);
+        expert_product<C>(q, p, a.k, at.rows, lds, sums);
     }
     if constexpr (OUT == kGateGrad) {
         float *const parts = reinterpret_cast<float *>(shared);      // [WP][BQ]
         if (a.partial) block_barrier();                              // the ring is read
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
-            const int m = (wq * TQ + t) * 16 + (lane & 15);
+            const int m = (t * C::WQ + wq) * 16 + (lane & 15);
             const bool in = m < at.rows;
             const int64_t row = at.start + (in ? m : 0);
             const float w = a.row_weights && in ? a.row_weights[row] : 1.0f;
@@ -201,7 +221,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
         const int64_t w_at = at.expert * w_rows;
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
-            const int m = (wq * TQ + t) * 16 + (lane & 15);
+            const int m = (t * C::WQ + wq) * 16 + (lane & 15);
             if (m >= at.rows) continue;
             const int64_t row = at.start + m;
             float xs = 1.0f;
@@ -278,7 +298,8 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(co
     const int place = static_cast<int>(tile % (down * across));
     const int q0 = place % down * C::BQ, p0 = place / down * C::BP;
     // no layout content sends a load out of the rows' buffers
-    int64_t start = a.seg.psum[expert], rows = a.seg.counts[expert];
+    int64_t start = __builtin_amdgcn_readfirstlane(a.seg.psum[expert]);
+    int64_t rows = __builtin_amdgcn_readfirstlane(a.seg.counts[expert]);
     if (start < 0 || start >= a.seg.capacity || rows < 0) start = rows = 0;
     if (rows > a.seg.capacity - start) rows = a.seg.capacity - start;
     const uint32_t lds = lds_address(shared);
@@ -289,11 +310,11 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(co
     p.init(static_cast<const char *>(a.x) + (GATHER ? 0 : start * a.k * 2),
            2 * static_cast<int64_t>(a.k), p0, a.k);
     if (GATHER) p.gather(a.seg.src_meta + start, a.seg.num_topk, a.seg.num_tokens);
-    tile_product<C>(q, p, static_cast<int>(rows), lds, sums);
+    tile_product<C, C::TQ>(q, p, static_cast<int>(rows), lds, sums);
     const int64_t base = static_cast<int64_t>(expert) * a.n;
 #pragma unroll
     for (int t = 0; t < C::TQ; ++t) {
-        const int j = q0 + (wq * C::TQ + t) * 16 + (lane & 15);
+        const int j = q0 + (t * C::WQ + wq) * 16 + (lane & 15);
         if (j >= a.n) continue;
 #pragma unroll
         for (int u = 0; u < C::TP; ++u) {

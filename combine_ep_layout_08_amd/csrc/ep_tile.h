@@ -47,6 +47,17 @@ struct Int8 {
     }
 };
 
+// A value that is the same in every lane, in a scalar register.
+__device__ inline int64_t uniform(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return static_cast<int64_t>(lo | static_cast<uint64_t>(hi) << 32);
+}
+
+__device__ inline const char *uniform(const void *p) {
+    return reinterpret_cast<const char *>(uniform(reinterpret_cast<int64_t>(p)));
+}
+
 // 16 bytes a lane from memory to LDS at `to` + 16 lane, `to` the same in all lanes.  The
 // compiler does not count these loads: wait_loads() does.  (Its builtin makes it wait for all
 // of them before any read of LDS.)  Lanes that are switched off write nothing.
@@ -96,7 +107,7 @@ __device__ inline int64_t token_of(const int32_t *src_meta, int64_t row, int top
 // from `base` (GATHER: its address).
 template <int R, int Threads, bool GATHER>
 struct RowsOperand {
-    static constexpr int kBytes = R * 128;
+    static constexpr int kBytes = R * 128, kReads = 1;       // of LDS, a fragment
     static constexpr int kLoads = kBytes / (Threads * 16) > 0 ? kBytes / (Threads * 16) : 1;
     static constexpr bool kPart = kBytes < Threads * 16;     // not every wave loads
     static_assert(kBytes % (Threads * 16) == 0 || kPart, "whole loads");
@@ -112,7 +123,7 @@ struct RowsOperand {
     template <typename RowOf>
     __device__ void init(const void *b, RowOf row_of) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        base = static_cast<const char *>(b);
+        base = uniform(b);
         unit = (threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7);
         to = wave * 1024;
         mine = !kPart || wave * 1024 < kBytes;
@@ -123,23 +134,37 @@ struct RowsOperand {
             else off[i] = static_cast<uint32_t>(at);
         }
     }
-    // The next chunk to `stage`, of which T has `channels`; what is missing is zeros.
-    template <typename T>
-    __device__ void load(uint32_t stage, int channels) {
+    // Loads a thread makes for the first `rows` rows.
+    static constexpr int loads(int rows) {
+        return kPart ? 1 : (rows * 8 + Threads - 1) / Threads;
+    }
+    // The next chunk to `stage`: the first N loads' rows, all of its channels.
+    template <int N>
+    __device__ void load(uint32_t stage) {
+        if (kPart && !mine) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (GATHER) {
+                load_lds(stage + to + i * Threads * 16, from[i]);
+                from[i] += 128;
+            } else {
+                load_lds(stage + to + i * Threads * 16, base, off[i]);
+            }
+        }
+        if (!GATHER) base += 128;
+    }
+    // The last chunk, of which T has `channels`; what is missing is zeros.
+    template <typename T, int N>
+    __device__ void load_end(uint32_t stage, int channels) {
         if (kPart && !mine) return;
         const bool in = unit * 16 < channels * T::kBytes;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
+        for (int i = 0; i < N; ++i) {
             const uint32_t at = stage + to + i * Threads * 16;
-            if (in) {
-                if (GATHER) load_lds(at, from[i]);
-                else load_lds(at, base, off[i]);
-            } else {
-                zero_lds(at + (threadIdx.x & 63) * 16);
-            }
-            if (GATHER) from[i] += 128;
+            if (!in) zero_lds(at + (threadIdx.x & 63) * 16);
+            else if (GATHER) load_lds(at, from[i]);
+            else load_lds(at, base, off[i]);
         }
-        if (!GATHER) base += 128;
     }
     // The wave's operand of a matrix instruction: rows 16 t .., channels of 64 bytes `half`.
     static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
@@ -153,6 +178,7 @@ struct RowsOperand {
 // thread's 16 bytes in load i from `base`, or its address (GATHER).
 template <int C, int Threads, bool GATHER>
 struct ColsOperand {
+    static constexpr int kReads = 2;                         // of LDS, a fragment
     static constexpr int kRow = 2 * C;                       // bytes of a channel
     static constexpr int kBytes = 64 * kRow;
     static constexpr int kLoads = kBytes / (Threads * 16);
@@ -173,8 +199,8 @@ struct ColsOperand {
 
     // Columns `first` .. of `cols` (in a row of `pitch` bytes) from channel 0 at `b`.
     __device__ void init(const void *b, int64_t row_pitch, int first, int cols) {
-        base = static_cast<const char *>(b);
-        pitch = row_pitch;
+        base = uniform(b);
+        pitch = uniform(row_pitch);
         to = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -190,24 +216,30 @@ struct ColsOperand {
         topk = k;
         tokens = t;
     }
-    // The next chunk to `stage`, of which `channels` are there; what is missing is zeros.
-    template <typename T>
-    __device__ void load(uint32_t stage, int channels) {
+    static constexpr int loads(int) { return kLoads; }
+    // The next chunk to `stage`, all of its channels.
+    template <int N>
+    __device__ void load(uint32_t stage) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t at = stage + to + i * Threads * 16;
-            const int ch = channel(i);
-            if (ch < channels) {
-                if (GATHER)
-                    load_lds(at, base + token_of(src_meta, ch, topk, tokens) * pitch + off[i]);
-                else
-                    load_lds(at, base, off[i]);
-            } else {
-                zero_lds(at + (threadIdx.x & 63) * 16);
-            }
-        }
+        for (int i = 0; i < N; ++i) load_one(stage + to + i * Threads * 16, i);
         if (GATHER) src_meta += 64;
         else base += 64 * pitch;
+    }
+    // The last chunk, of which `channels` are there; what is missing is zeros.
+    template <typename T, int N>
+    __device__ void load_end(uint32_t stage, int channels) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = stage + to + i * Threads * 16;
+            if (channel(i) < channels) load_one(at, i);
+            else zero_lds(at + (threadIdx.x & 63) * 16);
+        }
+    }
+    __device__ void load_one(uint32_t at, int i) {
+        if (GATHER)
+            load_lds(at, base + token_of(src_meta, channel(i), topk, tokens) * pitch + off[i]);
+        else
+            load_lds(at, base, off[i]);
     }
     static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
         const int lane = threadIdx.x & 63, j = lane & 15;
@@ -228,6 +260,25 @@ struct ColsOperand {
 };
 
 // ---------------------------------------------------------------- main loop
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// Spreads R reads of LDS over M matrix instructions of the same stretch of code.
+template <int M, int R>
+__device__ inline void interleave() {
+    constexpr int kMfma = 0x008, kRead = 0x100;
+    constexpr int each = M >= R ? 1 : (R + M - 1) / M;       // reads at a time
+    constexpr int times = R / each;
+    constexpr int per = M / (times > 0 ? times : 1) > 0 ? M / (times > 0 ? times : 1) : 1;
+#pragma unroll
+    for (int i = 0; i < times; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kRead, each, 0);
+        __builtin_amdgcn_sched_group_barrier(kMfma, per, 0);
+    }
+}
+
 // WQ x WP waves, each TQ x TP tiles of 16 x 16; S chunks in the ring.
 template <typename T, int BQ_, int BP_, int WQ_, int WP_, int S_>
 struct Tile {
@@ -244,59 +295,84 @@ struct Tile {
     static constexpr int kLds = kStage * S;
 };
 
-// Sums of the tile over `channels` channels.  `lds`: kLds bytes; when this returns a wave may
-// still be reading them.
-template <typename C, typename Q, typename P>
+// Sums of the tile over `channels` channels, of its first TA row tiles a wave (a wave has row
+// tiles wq, WQ + wq, 2 WQ + wq ..).  `lds`: kLds bytes; when this returns a wave may still be
+// reading them.
+//
+// A chunk is two matrix instructions deep.  While the first half of chunk c is multiplied its
+// second half is read from LDS; then comes the chunk's one barrier (chunk c is read by all, chunk
+// c + 1 has come), the first half of chunk c + 1 is read and the loads of chunk c + S set out into
+// the room of chunk c while the second half is multiplied.
+template <typename C, int TA, typename Q, typename P>
 __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
                                     typename C::Sums &sums) {
-    constexpr int S = C::S, kPerChunk = 128 / C::Type::kBytes;
-    constexpr int kLoads = Q::kLoads + P::kLoads;
-    static_assert(!P::kPart, "every wave loads of P");
+    typedef typename C::Type T;
+    constexpr int S = C::S, TP = C::TP, kPerChunk = 128 / T::kBytes;
+    constexpr int NQ = Q::loads(16 * C::WQ * TA), NP = P::kLoads;
+    static_assert(!P::kPart && TA <= C::TQ, "every wave loads of P");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wq = wave / C::WP, wp = wave % C::WP;
-    const int chunks = (channels + kPerChunk - 1) / kPerChunk;
+    const int chunks = (channels + kPerChunk - 1) / kPerChunk, whole = channels / kPerChunk;
 #pragma unroll
     for (int a = 0; a < C::TQ; ++a)
 #pragma unroll
-        for (int b = 0; b < C::TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
+        for (int b = 0; b < TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
+    if (chunks == 0) return;
     auto load = [&](int chunk, uint32_t stage) {
-        const int left = channels - chunk * kPerChunk;
-        q.template load<typename C::Type>(stage, left);
-        p.template load<typename C::Type>(stage + C::BQ * 128, left);
+        if (chunk < whole) {
+            q.template load<NQ>(stage);
+            p.template load<NP>(stage + C::BQ * 128);
+        } else if (chunk < chunks) {
+            q.template load_end<T, NQ>(stage, channels - chunk * kPerChunk);
+            p.template load_end<T, NP>(stage + C::BQ * 128, channels - chunk * kPerChunk);
+        }
     };
-    uint32_t head = lds, tail = lds;         // stages to load next, to compute on next
-    auto next = [&](uint32_t s) { return s + C::kStage == lds + C::kLds ? lds : s + C::kStage; };
+    // Until chunk c has come, c + `behind` having been the last to set out: only whole chunks
+    // have a known number of loads.
+    auto arrived = [&](int c, auto behind) {
+        constexpr int B = decltype(behind)::value;
+        if (c + B >= whole) wait_loads<0>();
+        else if (Q::kPart && !q.mine) wait_loads<B * NP>();
+        else wait_loads<B * (NQ + NP)>();
+    };
+    struct Half {
+        u32x4 q[TA], p[TP];
+    };
+    auto read = [&](Half &f, uint32_t stage, int half) {
 #pragma unroll
-    for (int i = 0; i + 1 < S; ++i)
-        if (i < chunks) {
-            load(i, head);
-            head = next(head);
-        }
+        for (int b = 0; b < TP; ++b)
+            f.p[b] = P::fragment(stage + C::BQ * 128, wp * TP + b, half);
+#pragma unroll
+        for (int a = 0; a < TA; ++a) f.q[a] = Q::fragment(stage, a * C::WQ + wq, half);
+    };
+    auto multiply = [&](const Half &f) {
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(f.p[b], f.q[a], sums.v[a][b]);
+    };
+    uint32_t at = lds;
+#pragma unroll
+    for (int i = 0; i < S; ++i) load(i, lds + i * C::kStage);
+    arrived(0, Int<S - 1>());
+    block_barrier();
+    Half first, second;
+    read(first, at, 0);
     for (int c = 0; c < chunks; ++c) {
-        // this chunk has come: at most the S - 2 behind it are still on their way, whole ones
-        if (c + S - 1 >= chunks) wait_loads<0>();
-        else if (Q::kPart && !q.mine) wait_loads<(S - 2) * P::kLoads>();
-        else wait_loads<(S - 2) * kLoads>();
+        read(second, at, 1);
+        multiply(first);
+        interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
+        __builtin_amdgcn_sched_barrier(0);
+        arrived(c + 1, Int<S - 2>());
         block_barrier();
-        if (c + S - 1 < chunks) {
-            load(c + S - 1, head);
-            head = next(head);
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            u32x4 fq[C::TQ], fp[C::TP];
-#pragma unroll
-            for (int b = 0; b < C::TP; ++b)
-                fp[b] = P::fragment(tail + C::BQ * 128, wp * C::TP + b, half);
-#pragma unroll
-            for (int a = 0; a < C::TQ; ++a) fq[a] = Q::fragment(tail, wq * C::TQ + a, half);
-#pragma unroll
-            for (int a = 0; a < C::TQ; ++a)
-#pragma unroll
-                for (int b = 0; b < C::TP; ++b)
-                    sums.v[a][b] = C::Type::mma(fp[b], fq[a], sums.v[a][b]);
-        }
-        tail = next(tail);
+        const uint32_t next = at + C::kStage == lds + C::kLds ? lds : at + C::kStage;
+        load(c + S, at);
+        // behind the last chunk nothing has come: what is read is not used
+        read(first, next, 0);
+        multiply(second);
+        interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
+        __builtin_amdgcn_sched_barrier(0);
+        at = next;
     }
 }
 

@@ -395,17 +395,17 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream) {
 template <typename T, int OUT, bool COLS>
 hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream) {
     const int64_t slots = slots_of(a.seg), experts = a.seg.num_experts;
-    if (slots > 64 * experts) return launch_expert<Tile<T, 256, 256, 2, 4, 2>, OUT, COLS>(a, stream);
-    if (slots > 16 * experts) return launch_expert<Tile<T, 64, 128, 2, 2, 3>, OUT, COLS>(a, stream);
+    if (slots > 64 * experts) return launch_expert<Tile<T, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
+    if (slots > 16 * experts) return launch_expert<Tile<T, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
     if constexpr (COLS)
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
     else
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
 }
 
 }  // namespace
 
-constexpr int kGateGradColumns = 128;
+constexpr int kGateGradColumns = 256;
 
 int gate_grad_tiles(int32_t inter) { return (inter + kGateGradColumns - 1) / kGateGradColumns; }
 
@@ -424,7 +424,7 @@ hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t stream) {
 
 hipError_t launch_expert_gate_grad(const ExpertArgs &a, float *grad_row_weights, const int32_t *dst,
                                    hipStream_t stream) {
-    hipError_t e = launch_expert<Tile<Bf16, 64, kGateGradColumns, 2, 2, 3>, kGateGrad, true>(a, stream);
+    hipError_t e = launch_expert<Tile<Bf16, 256, kGateGradColumns, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
     if (e != hipSuccess || !grad_row_weights) return e;
     const int64_t slots = slots_of(a.seg), blocks = (slots + 255) / 256;
     row_sums_kernel<<<static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
@@ -438,7 +438,7 @@ hipError_t launch_expert_grad_rows(const ExpertArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
-    typedef Tile<Bf16, 256, 256, 2, 4, 2> C;
+    typedef Tile<Bf16, 256, 256, 2, 4, 2, 3> C;
     const int64_t tiles = static_cast<int64_t>(a.seg.num_experts) * ((a.n + C::BQ - 1) / C::BQ) *
                           ((a.k + C::BP - 1) / C::BP);
     if (a.f32)

@@ -279,11 +279,13 @@ __device__ inline void interleave() {
     }
 }
 
-// WQ x WP waves, each TQ x TP tiles of 16 x 16; S chunks in the ring.
-template <typename T, int BQ_, int BP_, int WQ_, int WP_, int S_>
+// WQ x WP waves, each TQ x TP tiles of 16 x 16; rings of SQ chunks of Q and SP of P, SP being SQ
+// or one more.
+template <typename T, int BQ_, int BP_, int WQ_, int WP_, int SQ_, int SP_>
 struct Tile {
     typedef T Type;
-    static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, S = S_;
+    static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, SQ = SQ_, SP = SP_;
+    static_assert(SQ >= 2 && (SP == SQ || SP == SQ + 1), "what the waits count on");
     static constexpr int TQ = BQ / 16 / WQ, TP = BP / 16 / WP;
     static constexpr int kThreads = 64 * WQ * WP;
     static constexpr int kBlocks = kThreads >= 512 ? 1 : 512 / kThreads;   // a compute unit: 256 registers
@@ -291,8 +293,9 @@ struct Tile {
     struct Sums {
         Acc v[TQ][TP];
     };
-    static constexpr int kStage = (BQ + BP) * 128;
-    static constexpr int kLds = kStage * S;
+    static constexpr int kStageQ = BQ * 128, kStageP = BP * 128;
+    static constexpr int kRingQ = SQ * kStageQ, kLds = kRingQ + SP * kStageP;
+    static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
 };
 
 // Sums of the tile over `channels` channels, of its first TA row tiles a wave (a wave has row
@@ -301,13 +304,13 @@ struct Tile {
 //
 // A chunk is two matrix instructions deep.  While the first half of chunk c is multiplied its
 // second half is read from LDS; then comes the chunk's one barrier (chunk c is read by all, chunk
-// c + 1 has come), the first half of chunk c + 1 is read and the loads of chunk c + S set out into
-// the room of chunk c while the second half is multiplied.
+// c + 1 has come), the first half of chunk c + 1 is read and the loads of chunks c + SQ and
+// c + SP set out into the room of chunk c while the second half is multiplied.
 template <typename C, int TA, typename Q, typename P>
 __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
                                     typename C::Sums &sums) {
     typedef typename C::Type T;
-    constexpr int S = C::S, TP = C::TP, kPerChunk = 128 / T::kBytes;
+    constexpr int TP = C::TP, kPerChunk = 128 / T::kBytes;
     constexpr int NQ = Q::loads(16 * C::WQ * TA), NP = P::kLoads;
     static_assert(!P::kPart && TA <= C::TQ, "every wave loads of P");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -318,32 +321,32 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
 #pragma unroll
         for (int b = 0; b < TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
     if (chunks == 0) return;
-    auto load = [&](int chunk, uint32_t stage) {
-        if (chunk < whole) {
-            q.template load<NQ>(stage);
-            p.template load<NP>(stage + C::BQ * 128);
-        } else if (chunk < chunks) {
-            q.template load_end<T, NQ>(stage, channels - chunk * kPerChunk);
-            p.template load_end<T, NP>(stage + C::BQ * 128, channels - chunk * kPerChunk);
-        }
+    const uint32_t ring_q = lds, ring_p = lds + C::kRingQ;
+    auto load_q = [&](int chunk, uint32_t stage) {
+        if (chunk < whole) q.template load<NQ>(stage);
+        else if (chunk < chunks) q.template load_end<T, NQ>(stage, channels - chunk * kPerChunk);
     };
-    // Until chunk c has come, c + `behind` having been the last to set out: only whole chunks
-    // have a known number of loads.
-    auto arrived = [&](int c, auto behind) {
-        constexpr int B = decltype(behind)::value;
-        if (c + B >= whole) wait_loads<0>();
-        else if (Q::kPart && !q.mine) wait_loads<B * NP>();
-        else wait_loads<B * (NQ + NP)>();
+    auto load_p = [&](int chunk, uint32_t stage) {
+        if (chunk < whole) p.template load<NP>(stage);
+        else if (chunk < chunks) p.template load_end<T, NP>(stage, channels - chunk * kPerChunk);
+    };
+    // Until chunk c has come.  Behind its loads SQ - 2 chunks of Q and SP - 2 of P set out, in the
+    // first wait one more (AHEAD); only whole chunks have a known number of loads.
+    auto arrived = [&](int c, auto ahead) {
+        constexpr int BQ = C::SQ - 2 + decltype(ahead)::value;
+        constexpr int BP = C::SP - 2 + decltype(ahead)::value;
+        if (c + BP >= whole) wait_loads<0>();
+        else if (Q::kPart && !q.mine) wait_loads<BP * NP>();
+        else wait_loads<BQ * NQ + BP * NP>();
     };
     struct Half {
         u32x4 q[TA], p[TP];
     };
-    auto read = [&](Half &f, uint32_t stage, int half) {
+    auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half) {
 #pragma unroll
-        for (int b = 0; b < TP; ++b)
-            f.p[b] = P::fragment(stage + C::BQ * 128, wp * TP + b, half);
+        for (int b = 0; b < TP; ++b) f.p[b] = P::fragment(stage_p, wp * TP + b, half);
 #pragma unroll
-        for (int a = 0; a < TA; ++a) f.q[a] = Q::fragment(stage, a * C::WQ + wq, half);
+        for (int a = 0; a < TA; ++a) f.q[a] = Q::fragment(stage_q, a * C::WQ + wq, half);
     };
     auto multiply = [&](const Half &f) {
 #pragma unroll
@@ -351,28 +354,33 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
 #pragma unroll
             for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(f.p[b], f.q[a], sums.v[a][b]);
     };
-    uint32_t at = lds;
+    // in the order of the loop: P's chunk ahead of Q's by SP - SQ
 #pragma unroll
-    for (int i = 0; i < S; ++i) load(i, lds + i * C::kStage);
-    arrived(0, Int<S - 1>());
+    for (int i = 0; i < C::SP; ++i) {
+        if (i >= C::SP - C::SQ) load_q(i - (C::SP - C::SQ), ring_q + (i - (C::SP - C::SQ)) * C::kStageQ);
+        load_p(i, ring_p + i * C::kStageP);
+    }
+    arrived(0, Int<1>());
     block_barrier();
+    uint32_t at_q = ring_q, at_p = ring_p;
     Half first, second;
-    read(first, at, 0);
+    read(first, at_q, at_p, 0);
     for (int c = 0; c < chunks; ++c) {
-        read(second, at, 1);
+        read(second, at_q, at_p, 1);
         multiply(first);
         interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
         __builtin_amdgcn_sched_barrier(0);
-        arrived(c + 1, Int<S - 2>());
+        arrived(c + 1, Int<0>());
         block_barrier();
-        const uint32_t next = at + C::kStage == lds + C::kLds ? lds : at + C::kStage;
-        load(c + S, at);
+        load_q(c + C::SQ, at_q);
+        load_p(c + C::SP, at_p);
+        at_q = at_q + C::kStageQ == ring_p ? ring_q : at_q + C::kStageQ;
+        at_p = at_p + C::kStageP == lds + C::kLds ? ring_p : at_p + C::kStageP;
         // behind the last chunk nothing has come: what is read is not used
-        read(first, next, 0);
+        read(first, at_q, at_p, 0);
         multiply(second);
         interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
         __builtin_amdgcn_sched_barrier(0);
-        at = next;
     }
 }
 

@@ -138,19 +138,17 @@ struct RowsOperand {
     static constexpr int loads(int rows) {
         return kPart ? 1 : (rows * 8 + Threads - 1) / Threads;
     }
-    // The next chunk to `stage`: the first N loads' rows, all of its channels.
-    template <int N>
-    __device__ void load(uint32_t stage) {
+    // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
+    __device__ void load(uint32_t stage, int i) {
         if (kPart && !mine) return;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (GATHER) {
-                load_lds(stage + to + i * Threads * 16, from[i]);
-                from[i] += 128;
-            } else {
-                load_lds(stage + to + i * Threads * 16, base, off[i]);
-            }
+        if (GATHER) {
+            load_lds(stage + to + i * Threads * 16, from[i]);
+            from[i] += 128;
+        } else {
+            load_lds(stage + to + i * Threads * 16, base, off[i]);
         }
+    }
+    __device__ void advance() {
         if (!GATHER) base += 128;
     }
     // The last chunk, of which T has `channels`; what is missing is zeros.
@@ -217,11 +215,9 @@ struct ColsOperand {
         tokens = t;
     }
     static constexpr int loads(int) { return kLoads; }
-    // The next chunk to `stage`, all of its channels.
-    template <int N>
-    __device__ void load(uint32_t stage) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) load_one(stage + to + i * Threads * 16, i);
+    // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
+    __device__ void load(uint32_t stage, int i) { load_one(stage + to + i * Threads * 16, i); }
+    __device__ void advance() {
         if (GATHER) src_meta += 64;
         else base += 64 * pitch;
     }
@@ -322,13 +318,15 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
         for (int b = 0; b < TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
     if (chunks == 0) return;
     const uint32_t ring_q = lds, ring_p = lds + C::kRingQ;
-    auto load_q = [&](int chunk, uint32_t stage) {
-        if (chunk < whole) q.template load<NQ>(stage);
-        else if (chunk < chunks) q.template load_end<T, NQ>(stage, channels - chunk * kPerChunk);
-    };
-    auto load_p = [&](int chunk, uint32_t stage) {
-        if (chunk < whole) p.template load<NP>(stage);
-        else if (chunk < chunks) p.template load_end<T, NP>(stage, channels - chunk * kPerChunk);
+    auto load = [&](auto &o, auto count, int chunk, uint32_t stage) {
+        constexpr int N = decltype(count)::value;
+        if (chunk < whole) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) o.load(stage, i);
+            o.advance();
+        } else if (chunk < chunks) {
+            o.template load_end<T, N>(stage, channels - chunk * kPerChunk);
+        }
     };
     // Until chunk c has come.  Behind its loads SQ - 2 chunks of Q and SP - 2 of P set out, in the
     // first wait one more (AHEAD); only whole chunks have a known number of loads.
@@ -342,46 +340,64 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
     struct Half {
         u32x4 q[TA], p[TP];
     };
-    auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half) {
-#pragma unroll
-        for (int b = 0; b < TP; ++b) f.p[b] = P::fragment(stage_p, wp * TP + b, half);
-#pragma unroll
-        for (int a = 0; a < TA; ++a) f.q[a] = Q::fragment(stage_q, a * C::WQ + wq, half);
+    auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) {
+        if (i < TP) f.p[i] = P::fragment(stage_p, wp * TP + i, half);
+        else f.q[i - TP] = Q::fragment(stage_q, (i - TP) * C::WQ + wq, half);
     };
-    auto multiply = [&](const Half &f) {
+    // Multiplies `now`, a row tile at a time, while `then` is read and, with LOAD, the N loads of
+    // a chunk set out: issued all at once they take the address unit 16 cycles each, in which
+    // nothing is multiplied.
+    auto step = [&](const Half &now, Half &then, uint32_t stage_q, uint32_t stage_p, int half,
+                    auto &o, auto count, uint32_t room, auto with) {
+        constexpr int N = decltype(count)::value, R = TP + TA;
 #pragma unroll
-        for (int a = 0; a < TA; ++a)
+        for (int a = 0; a < TA; ++a) {
+            if constexpr (decltype(with)::value != 0) {
 #pragma unroll
-            for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(f.p[b], f.q[a], sums.v[a][b]);
+                for (int i = a * N / TA; i < (a + 1) * N / TA; ++i) o.load(room, i);
+                if (a == TA - 1) o.advance();
+            }
+#pragma unroll
+            for (int i = a * R / TA; i < (a + 1) * R / TA; ++i)
+                read(then, stage_q, stage_p, half, i);
+#pragma unroll
+            for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(now.p[b], now.q[a], sums.v[a][b]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     // in the order of the loop: P's chunk ahead of Q's by SP - SQ
+    constexpr int D = C::SP - C::SQ;
 #pragma unroll
     for (int i = 0; i < C::SP; ++i) {
-        if (i >= C::SP - C::SQ) load_q(i - (C::SP - C::SQ), ring_q + (i - (C::SP - C::SQ)) * C::kStageQ);
-        load_p(i, ring_p + i * C::kStageP);
+        if (i >= D) load(q, Int<NQ>(), i - D, ring_q + (i - D) * C::kStageQ);
+        load(p, Int<NP>(), i, ring_p + i * C::kStageP);
     }
     arrived(0, Int<1>());
     block_barrier();
-    uint32_t at_q = ring_q, at_p = ring_p;
+    uint32_t at_q = ring_q, at_p = ring_p, free_p = 0;
     Half first, second;
-    read(first, at_q, at_p, 0);
-    for (int c = 0; c < chunks; ++c) {
-        read(second, at_q, at_p, 1);
-        multiply(first);
-        interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < TP + TA; ++i) read(first, at_q, at_p, 0, i);
+    // `steady`: the chunks that set out are whole ones
+    auto chunk = [&](int c, auto steady) {
+        constexpr bool kSteady = decltype(steady)::value != 0;
+        if (!kSteady && c > 0) load(p, Int<NP>(), c - 1 + C::SP, free_p);
+        if (kSteady && c > 0) step(first, second, at_q, at_p, 1, p, Int<NP>(), free_p, Int<1>());
+        else step(first, second, at_q, at_p, 1, p, Int<NP>(), free_p, Int<0>());
         arrived(c + 1, Int<0>());
         block_barrier();
-        load_q(c + C::SQ, at_q);
-        load_p(c + C::SP, at_p);
+        const uint32_t free_q = at_q;
+        free_p = at_p;
+        if (!kSteady) load(q, Int<NQ>(), c + C::SQ, free_q);
         at_q = at_q + C::kStageQ == ring_p ? ring_q : at_q + C::kStageQ;
         at_p = at_p + C::kStageP == lds + C::kLds ? ring_p : at_p + C::kStageP;
         // behind the last chunk nothing has come: what is read is not used
-        read(first, at_q, at_p, 0);
-        multiply(second);
-        interleave<TA * TP, Q::kReads * TA + P::kReads * TP>();
-        __builtin_amdgcn_sched_barrier(0);
-    }
+        step(second, first, at_q, at_p, 0, q, Int<NQ>(), free_q, Int<kSteady>());
+    };
+    int c = 0;
+    chunk(c++, Int<0>());
+    for (; c + C::SQ < whole && c + C::SP <= whole; ++c) chunk(c, Int<1>());
+    for (; c < chunks; ++c) chunk(c, Int<0>());
 }
 
 }  // namespace ep

@@ -86,19 +86,15 @@ __device__ inline bool block_tile(const Segments &seg, int64_t first, int per, i
     return true;
 }
 
-// The tile's sums, without the row tiles that it has no rows for.
+// A tile that is full or nearly so has code of its own: what decides on the row tiles to leave out
+// costs 2 %.
 template <typename C, typename Q, typename P>
 __device__ inline void expert_product(Q &q, P &p, int channels, int rows, uint32_t lds,
                                       typename C::Sums &sums) {
-    if constexpr (C::TQ == 8) {
-        const int tiles = (rows + 16 * C::WQ - 1) / (16 * C::WQ);
-        if (tiles > 6) tile_product<C, 8>(q, p, channels, lds, sums);
-        else if (tiles > 4) tile_product<C, 6>(q, p, channels, lds, sums);
-        else if (tiles > 2) tile_product<C, 4>(q, p, channels, lds, sums);
-        else tile_product<C, 2>(q, p, channels, lds, sums);
-    } else {
-        tile_product<C, C::TQ>(q, p, channels, lds, sums);
-    }
+    if (C::TQ <= 2 || rows > C::M * C::WQ * (C::TQ - 2))
+        tile_product<C, true>(q, p, channels, rows, lds, sums);
+    else
+        tile_product<C, false>(q, p, channels, rows, lds, sums);
 }
 
 enum Out { kPlain, kGated, kGateGrad };
@@ -109,16 +105,17 @@ enum Out { kPlain, kGated, kGateGrad };
 //              holds both: their activation is what is stored
 //   kGateGrad  the sums are the gradient of the activation; gate and up are read, their
 //              gradients stored
-// The sums lie in the lanes as four consecutive outputs of one row.  Where the weights are in
-// rows, which weight goes to which place of the tile is free: a lane's tiles are made
-// consecutive, and it stores 8 outputs (16 bytes) at a time.
+// The sums lie in the lanes as groups of four consecutive outputs of one row.  Where the weights
+// are in rows, which weight goes to which place of the tile is free: a lane's outputs are made
+// consecutive, and it stores 8 of them (16 bytes) at a time.
 template <typename C, int OUT, bool COLS, bool GATHER>
 __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const ExpertArgs a, int64_t first) {
     constexpr bool I8 = C::Type::kBytes == 1;
     constexpr int TQ = C::TQ, TP = C::TP;
     constexpr int BP = OUT == kGated ? C::BP / 2 : C::BP;    // outputs of a tile
     extern __shared__ u32x4 shared[];
-    const int lane = threadIdx.x & 63, q4 = lane >> 4;
+    constexpr int M = C::M, kGroups = C::Type::kGroups;
+    const int lane = threadIdx.x & 63, part = lane / M;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wq = wave / C::WP, wp = wave % C::WP;
     const int across = (a.n + BP - 1) / BP;
@@ -148,12 +145,13 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
     } else {
         RowsOperand<C::BP, C::kThreads, false> p;
         const char *w = static_cast<const char *>(a.w) + at.expert * w_rows * pitch;
-        // LDS row (wave, tile, i) has output (i / 4) 4 TP + 4 tile + i % 4 of the wave's; gated,
-        // the tiles of the upper half are up's.
+        // LDS row i of the wave's tile t is what lane part i / 4 % (64 / M) has in group i M / 256;
+        // gated, the tiles of the upper half are up's.
         p.init(w, [&](int r) {
-            constexpr int G = OUT == kGated ? TP / 2 : TP;
-            const int i = r % 16, t = r / 16 % TP;
-            int j = p0 + r / (16 * TP) * 16 * G + i / 4 * 4 * G + t % G * 4 + i % 4;
+            constexpr int G = OUT == kGated ? TP / 2 : TP, L = 64 / M;
+            const int i = r % M, t = r / M % TP;
+            int j = p0 + r / (M * TP) * M * G + i / 4 % L * 4 * kGroups * G +
+                    t % G * 4 * kGroups + i / (4 * L) * 4 + i % 4;
             j = j < a.n ? j : a.n - 1;                       // computed on, and not stored
             return (j + (t < G ? 0 : a.n)) * pitch;
         });
@@ -164,14 +162,14 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
         if (a.partial) block_barrier();                              // the ring is read
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
-            const int m = (t * C::WQ + wq) * 16 + (lane & 15);
+            const int m = (t * C::WQ + wq) * M + lane % M;
             const bool in = m < at.rows;
             const int64_t row = at.start + (in ? m : 0);
             const float w = a.row_weights && in ? a.row_weights[row] : 1.0f;
             float total = 0.0f;
 #pragma unroll
-            for (int u = 0; u < TP; ++u) {
-                const int col = p0 + (wp * TP + u) * 16 + 4 * q4;
+            for (int u = 0; u < TP * kGroups; ++u) {
+                const int col = p0 + (wp * TP + u / kGroups) * M + u % kGroups * 8 + 4 * part;
                 if (!in || col >= a.n) continue;
                 const int64_t gate_at = row * 2 * a.n + col;
                 const uint16_t *gu = static_cast<const uint16_t *>(a.gate_up) + gate_at;
@@ -182,7 +180,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
                 float og[4], ou[4], oh[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float gh = static_cast<float>(sums.v[t][u][i]);
+                    const float gh = sums.v[t][u / kGroups][u % kGroups * 4 + i];
                     const float s = sigmoid(g[i]);
                     const float silu = g[i] * s, whole = silu * up[i];
                     total = __builtin_fmaf(gh, whole, total);
@@ -200,9 +198,9 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
                         u32x2{pack2(oh[0], oh[1]), pack2(oh[2], oh[3])};
             }
             if (a.partial) {
-                total += __shfl_xor(total, 16);
+                if (M == 16) total += __shfl_xor(total, 16);
                 total += __shfl_xor(total, 32);
-                if (lane < 16) parts[wp * C::BQ + m] = total;
+                if (lane < M) parts[wp * C::BQ + m] = total;
             }
         }
         if (!a.partial) return;
@@ -216,12 +214,13 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
         return;
     } else {
         constexpr int G = OUT == kGated ? TP / 2 : TP;       // tiles of outputs a lane has
-        constexpr int V = COLS ? 4 : 4 * G;                  // consecutive outputs
+        constexpr int R = 4 * kGroups;                       // outputs of a tile a lane has
+        constexpr int V = COLS ? 4 : R * G;                  // consecutive outputs
         constexpr int U = V < 8 ? V : 8;                     // stored at a time
         const int64_t w_at = at.expert * w_rows;
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
-            const int m = (t * C::WQ + wq) * 16 + (lane & 15);
+            const int m = (t * C::WQ + wq) * M + lane % M;
             if (m >= at.rows) continue;
             const int64_t row = at.start + m;
             float xs = 1.0f;
@@ -231,16 +230,16 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
                                       : row];
             const float w = OUT == kGated && a.row_weights ? a.row_weights[row] : 1.0f;
 #pragma unroll
-            for (int u = 0; u < 4 * G; u += U) {             // of the lane's outputs
-                const int col = COLS ? p0 + (wp * TP + u / 4) * 16 + 4 * q4
-                                     : p0 + wp * 16 * G + q4 * 4 * G + u;
+            for (int u = 0; u < R * G; u += U) {             // of the lane's outputs
+                const int col = COLS ? p0 + (wp * TP + u / R) * M + u % R * 2 + 4 * part
+                                     : p0 + wp * M * G + part * R * G + u;
                 if (col >= a.n) continue;
                 float v[U], up[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    v[i] = static_cast<float>(sums.v[t][(u + i) / 4][i % 4]);
+                    v[i] = static_cast<float>(sums.v[t][(u + i) / R][(u + i) % R]);
                     if (OUT == kGated)
-                        up[i] = static_cast<float>(sums.v[t][(G + (u + i) / 4) % TP][i % 4]);
+                        up[i] = static_cast<float>(sums.v[t][(G + (u + i) / R) % TP][(u + i) % R]);
                 }
                 if (I8) {
 #pragma unroll
@@ -285,15 +284,16 @@ template <typename C, bool GATHER, bool F32>
 __global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(const GradWeightArgs a,
                                                                      int64_t first) {
     extern __shared__ u32x4 shared[];
-    const int lane = threadIdx.x & 63, q4 = lane >> 4;
+    constexpr int M = C::M, kGroups = C::Type::kGroups;
+    const int lane = threadIdx.x & 63, part = lane / M;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wq = wave / C::WP, wp = wave % C::WP;
     const int down = (a.n + C::BQ - 1) / C::BQ, across = (a.k + C::BP - 1) / C::BP;
     const uint32_t bits = static_cast<uint32_t>(a.seg.scalars[EP_SCALAR_ERROR_BITS]);
     const int64_t all = static_cast<int64_t>(a.seg.num_experts) * down * across;
-    const int64_t id = first + blockIdx.x, part = (all + 7) / 8;
-    const int64_t tile = (id & 7) * part + (id >> 3);
-    if ((id >> 3) >= part || tile >= all || (bits & EP_ERRBIT_FATAL)) return;
+    const int64_t id = first + blockIdx.x, share = (all + 7) / 8;
+    const int64_t tile = (id & 7) * share + (id >> 3);
+    if ((id >> 3) >= share || tile >= all || (bits & EP_ERRBIT_FATAL)) return;
     const int expert = static_cast<int>(tile / (down * across));
     const int place = static_cast<int>(tile % (down * across));
     const int q0 = place % down * C::BQ, p0 = place / down * C::BP;
@@ -310,17 +310,19 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(co
     p.init(static_cast<const char *>(a.x) + (GATHER ? 0 : start * a.k * 2),
            2 * static_cast<int64_t>(a.k), p0, a.k);
     if (GATHER) p.gather(a.seg.src_meta + start, a.seg.num_topk, a.seg.num_tokens);
-    tile_product<C, C::TQ>(q, p, static_cast<int>(rows), lds, sums);
+    tile_product<C, true>(q, p, static_cast<int>(rows), C::BQ, lds, sums);
     const int64_t base = static_cast<int64_t>(expert) * a.n;
 #pragma unroll
     for (int t = 0; t < C::TQ; ++t) {
-        const int j = q0 + (t * C::WQ + wq) * 16 + (lane & 15);
+        const int j = q0 + (t * C::WQ + wq) * M + lane % M;
         if (j >= a.n) continue;
 #pragma unroll
-        for (int u = 0; u < C::TP; ++u) {
-            const int c = p0 + (wp * C::TP + u) * 16 + 4 * q4;
+        for (int u = 0; u < C::TP * kGroups; ++u) {
+            const int c = p0 + (wp * C::TP + u / kGroups) * M + u % kGroups * 8 + 4 * part;
             if (c >= a.k) continue;
-            const f32x4 v = sums.v[t][u];
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = sums.v[t][u / kGroups][u % kGroups * 4 + i];
             const int64_t to = (base + j) * a.k + c;
             if (F32)
                 *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to) = v;
@@ -392,15 +394,15 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream) {
     return launch_tiles<C>(expert_kernel<C, OUT, COLS, false>, a, tiles, stream);
 }
 
-template <typename T, int OUT, bool COLS>
+template <template <int> class T, int OUT, bool COLS>
 hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream) {
     const int64_t slots = slots_of(a.seg), experts = a.seg.num_experts;
-    if (slots > 64 * experts) return launch_expert<Tile<T, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
-    if (slots > 16 * experts) return launch_expert<Tile<T, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
+    if (slots > 64 * experts) return launch_expert<Tile<T<16>, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
+    if (slots > 16 * experts) return launch_expert<Tile<T<16>, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
     if constexpr (COLS)
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T<16>, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
     else
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T<16>, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
 }
 
 }  // namespace
@@ -424,7 +426,7 @@ hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t stream) {
 
 hipError_t launch_expert_gate_grad(const ExpertArgs &a, float *grad_row_weights, const int32_t *dst,
                                    hipStream_t stream) {
-    hipError_t e = launch_expert<Tile<Bf16, 256, kGateGradColumns, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
+    hipError_t e = launch_expert<Tile<Bf16<16>, 256, kGateGradColumns, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
     if (e != hipSuccess || !grad_row_weights) return e;
     const int64_t slots = slots_of(a.seg), blocks = (slots + 255) / 256;
     row_sums_kernel<<<static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
@@ -438,7 +440,7 @@ hipError_t launch_expert_grad_rows(const ExpertArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
-    typedef Tile<Bf16, 256, 256, 2, 4, 2, 3> C;
+    typedef Tile<Bf16<16>, 256, 256, 2, 4, 2, 3> C;
     const int64_t tiles = static_cast<int64_t>(a.seg.num_experts) * ((a.n + C::BQ - 1) / C::BQ) *
                           ((a.k + C::BP - 1) / C::BP);
     if (a.f32)

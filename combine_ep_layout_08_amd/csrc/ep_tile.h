@@ -7,8 +7,8 @@
 // expert's rows).  A chunk is 128 bytes of channels: 64 in bf16, 128 in int8.
 //
 // Chunks go from memory straight to LDS (global_load_lds, 16 bytes a lane), `S` of them in a
-// ring.  Rows operands: an LDS row is 128 bytes, its 16-byte units permuted by u ^ (row % 8), so
-// that the 16 rows a matrix instruction reads are in different banks.  Cols operands: an LDS
+// ring.  Rows operands: an LDS row is 128 bytes, its 16-byte units permuted by the row's number, so
+// that the rows which LDS serves together are in different banks.  Cols operands: an LDS
 // row is one channel's BQ or BP values; ds_read_b64_tr_b16 hands each lane the four channels of
 // its own column.  The permutations are made by the addresses that the lanes load from, as the
 // load's place in LDS is fixed by the lane.
@@ -25,25 +25,29 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 #define EP_LDS __attribute__((address_space(3)))
 
-// 16 x 16 outputs of 64 bytes of channels: lane l holds p = l % 16 of the first operand, q =
-// l % 16 of the second, the 16 bytes of channels at 16 (l / 16) of both, and the outputs
-// p = 4 (l / 16) + i of q = l % 16.
+// Matrix instructions of M x M outputs.  Lane l holds p = l % M of the first operand, q = l % M
+// of the second, 16 bytes of channels at 16 (l / M) of both, and four consecutive outputs in
+// each of `groups` groups: p = 4 (64 / M) g + 4 (l / M) + i of q = l % M.
+template <int M_>
 struct Bf16 {
-    typedef f32x4 Acc;
-    static constexpr int kBytes = 2;
+    static constexpr int M = M_, kBytes = 2, kGroups = M * M / 256;
+    typedef float Acc __attribute__((ext_vector_type(4 * kGroups)));
     static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p),
-                                                       __builtin_bit_cast(bf16x8, q), c, 0, 0, 0);
+        const bf16x8 a = __builtin_bit_cast(bf16x8, p), b = __builtin_bit_cast(bf16x8, q);
+        if constexpr (M == 16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
 };
 
 // Sums of 32768 products of codes stay below 2^30: nothing is rounded.
+template <int M_>
 struct Int8 {
-    typedef i32x4 Acc;
-    static constexpr int kBytes = 1;
+    static constexpr int M = M_, kBytes = 1, kGroups = M * M / 256;
+    typedef int32_t Acc __attribute__((ext_vector_type(4 * kGroups)));
     static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, p),
-                                                     __builtin_bit_cast(i32x4, q), c, 0, 0, 0);
+        const i32x4 a = __builtin_bit_cast(i32x4, p), b = __builtin_bit_cast(i32x4, q);
+        if constexpr (M == 16) return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+        else return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
     }
 };
 
@@ -107,7 +111,7 @@ __device__ inline int64_t token_of(const int32_t *src_meta, int64_t row, int top
 // from `base` (GATHER: its address).
 template <int R, int Threads, bool GATHER>
 struct RowsOperand {
-    static constexpr int kBytes = R * 128, kReads = 1;       // of LDS, a fragment
+    static constexpr int kBytes = R * 128;
     static constexpr int kLoads = kBytes / (Threads * 16) > 0 ? kBytes / (Threads * 16) : 1;
     static constexpr bool kPart = kBytes < Threads * 16;     // not every wave loads
     static_assert(kBytes % (Threads * 16) == 0 || kPart, "whole loads");
@@ -119,12 +123,13 @@ struct RowsOperand {
     bool mine;
 
     static __device__ int row(int i) { return i * (Threads / 8) + threadIdx.x / 8; }
+    static __device__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
 
     template <typename RowOf>
     __device__ void init(const void *b, RowOf row_of) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         base = uniform(b);
-        unit = (threadIdx.x & 7) ^ ((threadIdx.x >> 3) & 7);
+        unit = (threadIdx.x & 7) ^ swizzle(threadIdx.x >> 3);
         to = wave * 1024;
         mine = !kPart || wave * 1024 < kBytes;
 #pragma unroll
@@ -133,10 +138,6 @@ struct RowsOperand {
             if (GATHER) from[i] = base + at;
             else off[i] = static_cast<uint32_t>(at);
         }
-    }
-    // Loads a thread makes for the first `rows` rows.
-    static constexpr int loads(int rows) {
-        return kPart ? 1 : (rows * 8 + Threads - 1) / Threads;
     }
     // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
     __device__ void load(uint32_t stage, int i) {
@@ -164,11 +165,12 @@ struct RowsOperand {
             else load_lds(at, base, off[i]);
         }
     }
-    // The wave's operand of a matrix instruction: rows 16 t .., channels of 64 bytes `half`.
-    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
+    // The wave's operand of a matrix instruction: rows M t .., the k-th 1024 / M bytes of channels.
+    template <int M>
+    static __device__ u32x4 fragment(uint32_t stage, int t, int k) {
         const int lane = threadIdx.x & 63;
-        return read_lds(stage + (16 * t + (lane & 15)) * 128 +
-                        (((half * 4 + (lane >> 4)) ^ (lane & 7)) << 4));
+        return read_lds(stage + (M * t + lane % M) * 128 +
+                        (((k * (64 / M) + lane / M) ^ swizzle(M * t + lane % M)) << 4));
     }
 };
 
@@ -176,7 +178,6 @@ struct RowsOperand {
 // thread's 16 bytes in load i from `base`, or its address (GATHER).
 template <int C, int Threads, bool GATHER>
 struct ColsOperand {
-    static constexpr int kReads = 2;                         // of LDS, a fragment
     static constexpr int kRow = 2 * C;                       // bytes of a channel
     static constexpr int kBytes = 64 * kRow;
     static constexpr int kLoads = kBytes / (Threads * 16);
@@ -214,7 +215,6 @@ struct ColsOperand {
         topk = k;
         tokens = t;
     }
-    static constexpr int loads(int) { return kLoads; }
     // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
     __device__ void load(uint32_t stage, int i) { load_one(stage + to + i * Threads * 16, i); }
     __device__ void advance() {
@@ -237,14 +237,16 @@ struct ColsOperand {
         else
             load_lds(at, base, off[i]);
     }
-    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
+    template <int M>
+    static __device__ u32x4 fragment(uint32_t stage, int t, int k) {
         const int lane = threadIdx.x & 63, j = lane & 15;
-        const int ch = half * 32 + (lane >> 4) * 8 + (j >> 2);
+        const int ch = k * (512 / M) + lane / M * 8 + (j >> 2);
+        const int unit = t * (M / 16) + lane % M / 16;       // 16 columns
         u32x4 v;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c = ch + 4 * i;
-            const uint32_t at = stage + c * kRow + ((t ^ swizzle(c)) << 5) + (j & 3) * 8;
+            const uint32_t at = stage + c * kRow + ((unit ^ swizzle(c)) << 5) + (j & 3) * 8;
             const u32x2 r = __builtin_bit_cast(
                 u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                            reinterpret_cast<EP_LDS s16x4 *>(static_cast<uintptr_t>(at))));
@@ -261,30 +263,16 @@ struct Int {
     static constexpr int value = N;
 };
 
-// Spreads R reads of LDS over M matrix instructions of the same stretch of code.
-template <int M, int R>
-__device__ inline void interleave() {
-    constexpr int kMfma = 0x008, kRead = 0x100;
-    constexpr int each = M >= R ? 1 : (R + M - 1) / M;       // reads at a time
-    constexpr int times = R / each;
-    constexpr int per = M / (times > 0 ? times : 1) > 0 ? M / (times > 0 ? times : 1) : 1;
-#pragma unroll
-    for (int i = 0; i < times; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kRead, each, 0);
-        __builtin_amdgcn_sched_group_barrier(kMfma, per, 0);
-    }
-}
-
-// WQ x WP waves, each TQ x TP tiles of 16 x 16; rings of SQ chunks of Q and SP of P, SP being SQ
+// WQ x WP waves, each TQ x TP matrix instructions; rings of SQ chunks of Q and SP of P, SP being SQ
 // or one more.
 template <typename T, int BQ_, int BP_, int WQ_, int WP_, int SQ_, int SP_>
 struct Tile {
     typedef T Type;
     static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, SQ = SQ_, SP = SP_;
     static_assert(SQ >= 2 && (SP == SQ || SP == SQ + 1), "what the waits count on");
-    static constexpr int TQ = BQ / 16 / WQ, TP = BP / 16 / WP;
+    static constexpr int M = T::M, TQ = BQ / M / WQ, TP = BP / M / WP;
     static constexpr int kThreads = 64 * WQ * WP;
-    static constexpr int kBlocks = kThreads >= 512 ? 1 : 512 / kThreads;   // a compute unit: 256 registers
+    static constexpr int kBlocks = kThreads >= 512 || TQ * TP > 32 ? 1 : 512 / kThreads;
     typedef typename T::Acc Acc;
     struct Sums {
         Acc v[TQ][TP];
@@ -294,28 +282,30 @@ struct Tile {
     static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
 };
 
-// Sums of the tile over `channels` channels, of its first TA row tiles a wave (a wave has row
-// tiles wq, WQ + wq, 2 WQ + wq ..).  `lds`: kLds bytes; when this returns a wave may still be
-// reading them.
+// Sums of the tile over `channels` channels, of its first `rows` rows at least (a wave has row
+// tiles wq, WQ + wq, 2 WQ + wq .., and leaves out pairs of them that are behind the rows; ALL: none).
+// `lds`: kLds bytes; when this returns a wave may still be reading them.
 //
-// A chunk is two matrix instructions deep.  While the first half of chunk c is multiplied its
-// second half is read from LDS; then comes the chunk's one barrier (chunk c is read by all, chunk
-// c + 1 has come), the first half of chunk c + 1 is read and the loads of chunks c + SQ and
-// c + SP set out into the room of chunk c while the second half is multiplied.
-template <typename C, int TA, typename Q, typename P>
-__device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
+// A chunk is multiplied in two halves of 64 bytes.  While the first half of chunk c is
+// multiplied its second half is read from LDS; then comes the chunk's one barrier (chunk c is
+// read by all, chunk c + 1 has come), and while the second half is multiplied the first half
+// of chunk c + 1 is read.  Q's loads of chunk c + SQ set out after the barrier, P's of chunk c + SP
+// half a chunk later, into the room of chunk c.
+template <typename C, bool ALL, typename Q, typename P>
+__device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t lds,
                                     typename C::Sums &sums) {
     typedef typename C::Type T;
-    constexpr int TP = C::TP, kPerChunk = 128 / T::kBytes;
-    constexpr int NQ = Q::loads(16 * C::WQ * TA), NP = P::kLoads;
-    static_assert(!P::kPart && TA <= C::TQ, "every wave loads of P");
+    constexpr int TQ = C::TQ, TP = C::TP, kPerChunk = 128 / T::kBytes;
+    constexpr int NQ = Q::kLoads, NP = P::kLoads;
+    static_assert(!P::kPart, "every wave loads of P");
+    const int active = (rows + C::M * C::WQ - 1) / (C::M * C::WQ);       // row tiles a wave
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wq = wave / C::WP, wp = wave % C::WP;
     const int chunks = (channels + kPerChunk - 1) / kPerChunk, whole = channels / kPerChunk;
 #pragma unroll
     for (int a = 0; a < C::TQ; ++a)
 #pragma unroll
-        for (int b = 0; b < TP; ++b) sums.v[a][b] = typename C::Acc{0, 0, 0, 0};
+        for (int b = 0; b < TP; ++b) sums.v[a][b] = typename C::Acc(0);
     if (chunks == 0) return;
     const uint32_t ring_q = lds, ring_p = lds + C::kRingQ;
     auto load = [&](auto &o, auto count, int chunk, uint32_t stage) {
@@ -337,31 +327,47 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
         else if (Q::kPart && !q.mine) wait_loads<BP * NP>();
         else wait_loads<BQ * NQ + BP * NP>();
     };
+    constexpr int K = C::M / 16;                 // matrix instructions of 64 bytes of channels
     struct Half {
-        u32x4 q[TA], p[TP];
+        u32x4 q[TQ][K], p[TP][K];
     };
     auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) {
-        if (i < TP) f.p[i] = P::fragment(stage_p, wp * TP + i, half);
-        else f.q[i - TP] = Q::fragment(stage_q, (i - TP) * C::WQ + wq, half);
+        const int k = i % K, t = i / K;
+        if (t < TP)
+            f.p[t][k] = P::template fragment<C::M>(stage_p, wp * TP + t, half * K + k);
+        else
+            f.q[t - TP][k] =
+                Q::template fragment<C::M>(stage_q, (t - TP) * C::WQ + wq, half * K + k);
     };
     // Multiplies `now`, a row tile at a time, while `then` is read and, with LOAD, the N loads of
-    // a chunk set out: issued all at once they take the address unit 16 cycles each, in which
-    // nothing is multiplied.
+    // a chunk set out.  Issued all at once the loads take the address unit 16 cycles each, in
+    // which nothing is multiplied; spread over all row tiles they come later (64 experts, 512 rows
+    // each, 7168 to 4096 bf16 channels: 1.55 ms, 1.53 spread over all, 1.51 over a half).
+    // Reads and loads of a tile that leaves out row tiles are made in those that are left.
     auto step = [&](const Half &now, Half &then, uint32_t stage_q, uint32_t stage_p, int half,
                     auto &o, auto count, uint32_t room, auto with) {
-        constexpr int N = decltype(count)::value, R = TP + TA;
+        constexpr int N = decltype(count)::value;
+        // row tiles in which loads set out; the ones that are never left out
+        constexpr int kMost = ALL ? (TQ + 1) / 2 : 2, kEarly = TQ < kMost ? TQ : kMost;
 #pragma unroll
-        for (int a = 0; a < TA; ++a) {
+        for (int a = 0; a < TQ; ++a) {
+            if (!ALL && a >= kEarly && a % 2 == 0 && a >= active) break;
             if constexpr (decltype(with)::value != 0) {
 #pragma unroll
-                for (int i = a * N / TA; i < (a + 1) * N / TA; ++i) o.load(room, i);
-                if (a == TA - 1) o.advance();
+                for (int i = 0; i < N; ++i)
+                    if (i * kEarly / N == a) o.load(room, i);
+                if (a == kEarly - 1) o.advance();
             }
 #pragma unroll
-            for (int i = a * R / TA; i < (a + 1) * R / TA; ++i)
-                read(then, stage_q, stage_p, half, i);
+            for (int i = 0; i < (TP + TQ) * K; ++i)
+                if (ALL ? i * TQ / ((TP + TQ) * K) == a
+                        : i < TP * K ? i * kEarly / (TP * K) == a : i / K - TP == a)
+                    read(then, stage_q, stage_p, half, i);
 #pragma unroll
-            for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(now.p[b], now.q[a], sums.v[a][b]);
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int b = 0; b < TP; ++b)
+                    sums.v[a][b] = T::mma(now.p[b][k], now.q[a][k], sums.v[a][b]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -377,7 +383,7 @@ __device__ inline void tile_product(Q &q, P &p, int channels, uint32_t lds,
     uint32_t at_q = ring_q, at_p = ring_p, free_p = 0;
     Half first, second;
 #pragma unroll
-    for (int i = 0; i < TP + TA; ++i) read(first, at_q, at_p, 0, i);
+    for (int i = 0; i < (TP + TQ) * K; ++i) read(first, at_q, at_p, 0, i);
     // `steady`: the chunks that set out are whole ones
     auto chunk = [&](int c, auto steady) {
         constexpr bool kSteady = decltype(steady)::value != 0;

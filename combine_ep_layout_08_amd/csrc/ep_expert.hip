@@ -1,5 +1,7 @@
 // The experts' products on gfx950 (include/ep_expert.h): int8 rows and weights, the bf16
 // gated feed-forward block, and its gradients.
+#include <type_traits>
+
 #include "ep_expert_internal.h"
 #include "ep_tile.h"
 
@@ -91,7 +93,7 @@ __device__ inline bool block_tile(const Segments &seg, int64_t first, int per, i
 template <typename C, typename Q, typename P>
 __device__ inline void expert_product(Q &q, P &p, int channels, int rows, uint32_t lds,
                                       typename C::Sums &sums) {
-    if (C::TQ <= 2 || rows > C::M * C::WQ * (C::TQ - 2))
+    if (C::TQ <= 2 || rows > 16 * C::WQ * (C::TQ - 2))
         tile_product<C, true>(q, p, channels, rows, lds, sums);
     else
         tile_product<C, false>(q, p, channels, rows, lds, sums);
@@ -105,150 +107,106 @@ enum Out { kPlain, kGated, kGateGrad };
 //              holds both: their activation is what is stored
 //   kGateGrad  the sums are the gradient of the activation; gate and up are read, their
 //              gradients stored
-// The sums lie in the lanes as groups of four consecutive outputs of one row.  Where the weights
-// are in rows, which weight goes to which place of the tile is free: a lane's outputs are made
-// consecutive, and it stores 8 of them (16 bytes) at a time.
+// The sums lie in the lanes as four outputs of one row from each matrix instruction.  Which weight
+// goes to which place of the tile is free: a lane's outputs are made consecutive, and it stores 8 of
+// them (16 bytes) at a time.
 template <typename C, int OUT, bool COLS, bool GATHER>
-__global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const ExpertArgs a, int64_t first) {
-    constexpr bool I8 = C::Type::kBytes == 1;
-    constexpr int TQ = C::TQ, TP = C::TP;
-    constexpr int BP = OUT == kGated ? C::BP / 2 : C::BP;    // outputs of a tile
-    extern __shared__ u32x4 shared[];
-    constexpr int M = C::M, kGroups = C::Type::kGroups;
-    const int lane = threadIdx.x & 63, part = lane / M;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wq = wave / C::WP, wp = wave % C::WP;
-    const int across = (a.n + BP - 1) / BP;
-    Place at;
-    if (!block_tile(a.seg, first, C::BQ, across, &at)) return;
-    const int p0 = at.column * BP;
-    const uint32_t lds = lds_address(shared);
-    typename C::Sums sums;
-    RowsOperand<C::BQ, C::kThreads, GATHER> q;
-    const int64_t pitch = static_cast<int64_t>(a.k) * C::Type::kBytes;
-    if (GATHER)
-        q.init(a.x, [&](int r) {
-            const int64_t row = at.start + (r < at.rows ? r : at.rows - 1);
-            return token_of(a.seg.src_meta, row, a.seg.num_topk, a.seg.num_tokens) * pitch;
-        });
-    else
-        q.init(static_cast<const char *>(a.x) + at.start * pitch, [&](int r) {
-            return (r < at.rows ? r : at.rows - 1) * pitch;
-        });
-    const int64_t w_rows = (OUT == kGated ? 2 : 1) * static_cast<int64_t>(a.n);
-    if constexpr (COLS) {
-        ColsOperand<C::BP, C::kThreads, false> p;
-        const char *w = static_cast<const char *>(a.w) +
-                        at.expert * static_cast<int64_t>(a.k) * a.n * 2;
-        p.init(w, 2 * static_cast<int64_t>(a.n), p0, a.n);
-        expert_product<C>(q, p, a.k, at.rows, lds, sums);
-    } else {
-        RowsOperand<C::BP, C::kThreads, false> p;
-        const char *w = static_cast<const char *>(a.w) + at.expert * w_rows * pitch;
-        // LDS row i of the wave's tile t is what lane part i / 4 % (64 / M) has in group i M / 256;
-        // gated, the tiles of the upper half are up's.
-        p.init(w, [&](int r) {
-            constexpr int G = OUT == kGated ? TP / 2 : TP, L = 64 / M;
-            const int i = r % M, t = r / M % TP;
-            int j = p0 + r / (M * TP) * M * G + i / 4 % L * 4 * kGroups * G +
-                    t % G * 4 * kGroups + i / (4 * L) * 4 + i % 4;
-            j = j < a.n ? j : a.n - 1;                       // computed on, and not stored
-            return (j + (t < G ? 0 : a.n)) * pitch;
-        });
-        expert_product<C>(q, p, a.k, at.rows, lds, sums);
+struct ExpertTile {
+    static constexpr bool I8 = C::Type::kBytes == 1;
+    static constexpr int TQ = C::TQ, TP = C::TP;
+    static constexpr int G = OUT == kGated ? TP / 2 : TP;    // matrix instructions of outputs
+    static constexpr int BP = 16 * C::WP * G;                // outputs of a tile
+    static constexpr int U = 4 * G < 8 ? 4 * G : 8;          // stored at a time
+    typedef RowsOperand<C::BQ, C::kThreads, GATHER> Q;
+    typedef std::conditional_t<COLS, ColsOperand<C::BP, C::kThreads, false, true>,
+                               RowsOperand<C::BP, C::kThreads, false>> P;
+    const ExpertArgs &a;
+    const Place &at;
+
+    __device__ void start_q(Q &q) const {
+        const int64_t pitch = static_cast<int64_t>(a.k) * C::Type::kBytes;
+        if constexpr (GATHER)
+            q.init(a.x, [&](int r) {
+                const int64_t row = at.start + (r < at.rows ? r : at.rows - 1);
+                return token_of(a.seg.src_meta, row, a.seg.num_topk, a.seg.num_tokens) * pitch;
+            });
+        else
+            q.init(static_cast<const char *>(a.x) + at.start * pitch, [&](int r) {
+                return (r < at.rows ? r : at.rows - 1) * pitch;
+            });
     }
-    if constexpr (OUT == kGateGrad) {
-        float *const parts = reinterpret_cast<float *>(shared);      // [WP][BQ]
-        if (a.partial) block_barrier();                              // the ring is read
+    __device__ void start_p(P &p) const {
+        const int64_t pitch = static_cast<int64_t>(a.k) * C::Type::kBytes;
+        const int p0 = at.column * BP;
+        const char *w = static_cast<const char *>(a.w) +
+                        at.expert * ((OUT == kGated ? 2 : 1) * static_cast<int64_t>(a.n) * pitch);
+        if constexpr (COLS) {
+            p.init(w, 2 * static_cast<int64_t>(a.n), p0, a.n);
+        } else {
+            // LDS row i of a wave's instruction t is what lane part i / 4 has of it; gated, the
+            // instructions of the upper half are up's
+            p.init(w, [&](int r) {
+                const int i = r % 16, t = r / 16 % TP;
+                int j = p0 + r / (16 * TP) * 16 * G + i / 4 * 4 * G + t % G * 4 + i % 4;
+                j = j < a.n ? j : a.n - 1;                   // computed on, and not stored
+                return (j + (t < G ? 0 : a.n)) * pitch;
+            });
+        }
+    }
+    static __device__ void store(void *to, int64_t place, const float *f) {
+        uint16_t *o = static_cast<uint16_t *>(to) + place;
+        if constexpr (U == 8)
+            *reinterpret_cast<u32x4 *>(o) = pack8(f);
+        else
+            *reinterpret_cast<u32x2 *>(o) = u32x2{pack2(f[0], f[1]), pack2(f[2], f[3])};
+    }
+    static __device__ void load(const void *from, int64_t place, float *f) {
+        const uint16_t *o = static_cast<const uint16_t *>(from) + place;
+        if constexpr (U == 8) {
+            unpack8(*reinterpret_cast<const u32x4 *>(o), f);
+        } else {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(o);
+            f[0] = bf16_lo(v.x);
+            f[1] = bf16_hi(v.x);
+            f[2] = bf16_lo(v.y);
+            f[3] = bf16_hi(v.y);
+        }
+    }
+    __device__ void finish(const typename C::Sums &sums) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int wq = wave / C::WP, wp = wave % C::WP, lane = threadIdx.x & 63;
+        const int col0 = at.column * BP + wp * 16 * G + (lane >> 4) * 4 * G;     // the lane's first output
+        const int64_t w_at = at.expert * ((OUT == kGated ? 2 : 1) * static_cast<int64_t>(a.n));
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
-            const int m = (t * C::WQ + wq) * M + lane % M;
+            const int m = (t * C::WQ + wq) * 16 + (lane & 15);
             const bool in = m < at.rows;
+            if (OUT != kGateGrad && !in) continue;
             const int64_t row = at.start + (in ? m : 0);
-            const float w = a.row_weights && in ? a.row_weights[row] : 1.0f;
-            float total = 0.0f;
-#pragma unroll
-            for (int u = 0; u < TP * kGroups; ++u) {
-                const int col = p0 + (wp * TP + u / kGroups) * M + u % kGroups * 8 + 4 * part;
-                if (!in || col >= a.n) continue;
-                const int64_t gate_at = row * 2 * a.n + col;
-                const uint16_t *gu = static_cast<const uint16_t *>(a.gate_up) + gate_at;
-                const u32x2 gv = *reinterpret_cast<const u32x2 *>(gu);
-                const u32x2 uv = *reinterpret_cast<const u32x2 *>(gu + a.n);
-                const float g[4] = {bf16_lo(gv.x), bf16_hi(gv.x), bf16_lo(gv.y), bf16_hi(gv.y)};
-                const float up[4] = {bf16_lo(uv.x), bf16_hi(uv.x), bf16_lo(uv.y), bf16_hi(uv.y)};
-                float og[4], ou[4], oh[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float gh = sums.v[t][u / kGroups][u % kGroups * 4 + i];
-                    const float s = sigmoid(g[i]);
-                    const float silu = g[i] * s, whole = silu * up[i];
-                    total = __builtin_fmaf(gh, whole, total);
-                    const float wg = w * gh;
-                    og[i] = wg * up[i] * (s * __builtin_fmaf(g[i], 1.0f - s, 1.0f));
-                    ou[i] = wg * silu;
-                    oh[i] = w * whole;
-                }
-                uint16_t *gg = static_cast<uint16_t *>(a.grad_gate_up) + gate_at;
-                *reinterpret_cast<u32x2 *>(gg) = u32x2{pack2(og[0], og[1]), pack2(og[2], og[3])};
-                *reinterpret_cast<u32x2 *>(gg + a.n) =
-                    u32x2{pack2(ou[0], ou[1]), pack2(ou[2], ou[3])};
-                if (a.out)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + row * a.n + col) =
-                        u32x2{pack2(oh[0], oh[1]), pack2(oh[2], oh[3])};
-            }
-            if (a.partial) {
-                if (M == 16) total += __shfl_xor(total, 16);
-                total += __shfl_xor(total, 32);
-                if (lane < M) parts[wp * C::BQ + m] = total;
-            }
-        }
-        if (!a.partial) return;
-        __syncthreads();
-        for (int m = threadIdx.x; m < at.rows; m += C::kThreads) {
-            float total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C::WP; ++i) total += parts[i * C::BQ + m];
-            a.partial[static_cast<int64_t>(at.column) * a.seg.capacity + at.start + m] = total;
-        }
-        return;
-    } else {
-        constexpr int G = OUT == kGated ? TP / 2 : TP;       // tiles of outputs a lane has
-        constexpr int R = 4 * kGroups;                       // outputs of a tile a lane has
-        constexpr int V = COLS ? 4 : R * G;                  // consecutive outputs
-        constexpr int U = V < 8 ? V : 8;                     // stored at a time
-        const int64_t w_at = at.expert * w_rows;
-#pragma unroll
-        for (int t = 0; t < TQ; ++t) {
-            const int m = (t * C::WQ + wq) * M + lane % M;
-            if (m >= at.rows) continue;
-            const int64_t row = at.start + m;
-            float xs = 1.0f;
+            float xs = 1.0f, w = 1.0f, total = 0.0f;
             if (I8)
                 xs = a.x_scale[GATHER ? token_of(a.seg.src_meta, row, a.seg.num_topk,
                                                  a.seg.num_tokens)
                                       : row];
-            const float w = OUT == kGated && a.row_weights ? a.row_weights[row] : 1.0f;
+            if (OUT != kPlain && a.row_weights && in) w = a.row_weights[row];
 #pragma unroll
-            for (int u = 0; u < R * G; u += U) {             // of the lane's outputs
-                const int col = COLS ? p0 + (wp * TP + u / R) * M + u % R * 2 + 4 * part
-                                     : p0 + wp * M * G + part * R * G + u;
-                if (col >= a.n) continue;
+            for (int u = 0; u < 4 * G; u += U) {             // of the lane's outputs
+                const int col = col0 + u;
+                if (!in || col >= a.n) continue;
                 float v[U], up[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    v[i] = static_cast<float>(sums.v[t][(u + i) / R][(u + i) % R]);
+                    v[i] = static_cast<float>(sums.v[t][(u + i) / 4][i % 4]);
                     if (OUT == kGated)
-                        up[i] = static_cast<float>(sums.v[t][(G + (u + i) / R) % TP][(u + i) % R]);
+                        up[i] = static_cast<float>(sums.v[t][(G + (u + i) / 4) % TP][i % 4]);
                 }
                 if (I8) {
 #pragma unroll
                     for (int i = 0; i < U; i += 4) {
-                        const f32x4 s =
-                            *reinterpret_cast<const f32x4 *>(a.w_scale + w_at + col + i);
+                        const float *ws = a.w_scale + w_at + col + i;
+                        const f32x4 s = *reinterpret_cast<const f32x4 *>(ws);
                         f32x4 su = s;
-                        if (OUT == kGated)
-                            su = *reinterpret_cast<const f32x4 *>(a.w_scale + w_at + a.n + col + i);
+                        if (OUT == kGated) su = *reinterpret_cast<const f32x4 *>(ws + a.n);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             v[i + j] = v[i + j] * xs * s[j];
@@ -256,14 +214,6 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
                         }
                     }
                 }
-                auto store = [&](void *to, int64_t place, const float *f) {
-                    uint16_t *o = static_cast<uint16_t *>(to) + place;
-                    if constexpr (U == 8)
-                        *reinterpret_cast<u32x4 *>(o) = pack8(f);
-                    else
-                        *reinterpret_cast<u32x2 *>(o) =
-                            u32x2{pack2(f[0], f[1]), pack2(f[2], f[3])};
-                };
                 if (OUT == kGated) {
                     if (a.saved) {
                         store(a.saved, row * 2 * a.n + col, v);
@@ -272,65 +222,165 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
 #pragma unroll
                     for (int i = 0; i < U; ++i) v[i] = v[i] * sigmoid(v[i]) * up[i] * w;
                 }
-                store(a.out, row * a.n + col, v);
+                if (OUT != kGateGrad) {
+                    store(a.out, row * a.n + col, v);
+                    continue;
+                }
+                float g[U], h[U], og[U], ou[U];
+                load(a.gate_up, row * 2 * a.n + col, g);
+                load(a.gate_up, row * 2 * a.n + a.n + col, up);
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const float s = sigmoid(g[i]);
+                    const float silu = g[i] * s, whole = silu * up[i];
+                    total = __builtin_fmaf(v[i], whole, total);
+                    const float wg = w * v[i];
+                    og[i] = wg * up[i] * (s * __builtin_fmaf(g[i], 1.0f - s, 1.0f));
+                    ou[i] = wg * silu;
+                    h[i] = w * whole;
+                }
+                store(a.grad_gate_up, row * 2 * a.n + col, og);
+                store(a.grad_gate_up, row * 2 * a.n + a.n + col, ou);
+                if (a.out) store(a.out, row * a.n + col, h);
+            }
+            if (OUT == kGateGrad && a.partial) {
+                total += __shfl_xor(total, 16);
+                total += __shfl_xor(total, 32);
+                if (lane < 16 && in)
+                    a.partial[(at.column * C::WP + wp) * a.seg.capacity + row] = total;
             }
         }
     }
+};
+
+template <typename C, int OUT, bool COLS, bool GATHER>
+__global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const ExpertArgs a,
+                                                                         int64_t first) {
+    typedef ExpertTile<C, OUT, COLS, GATHER> E;
+    extern __shared__ u32x4 shared[];
+    Place at;
+    if (!block_tile(a.seg, first, C::BQ, (a.n + E::BP - 1) / E::BP, &at)) return;
+    const E tile{a, at};
+    typename E::Q q;
+    typename E::P p;
+    typename C::Sums sums;
+    tile.start_q(q);
+    tile.start_p(p);
+    expert_product<C>(q, p, a.k, at.rows, lds_address(shared), sums);
+    tile.finish(sums);
 }
 
 // Gradient of the weights: out[e][j, c] = sum over the expert's rows of g[r, j] x[r, c].  P are
 // the columns of x, Q those of g, the rows what is summed.
 template <typename C, bool GATHER, bool F32>
-__global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(const GradWeightArgs a,
-                                                                     int64_t first) {
-    extern __shared__ u32x4 shared[];
-    constexpr int M = C::M, kGroups = C::Type::kGroups;
-    const int lane = threadIdx.x & 63, part = lane / M;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wq = wave / C::WP, wp = wave % C::WP;
-    const int down = (a.n + C::BQ - 1) / C::BQ, across = (a.k + C::BP - 1) / C::BP;
-    const uint32_t bits = static_cast<uint32_t>(a.seg.scalars[EP_SCALAR_ERROR_BITS]);
-    const int64_t all = static_cast<int64_t>(a.seg.num_experts) * down * across;
-    const int64_t id = first + blockIdx.x, share = (all + 7) / 8;
-    const int64_t tile = (id & 7) * share + (id >> 3);
-    if ((id >> 3) >= share || tile >= all || (bits & EP_ERRBIT_FATAL)) return;
-    const int expert = static_cast<int>(tile / (down * across));
-    const int place = static_cast<int>(tile % (down * across));
-    const int q0 = place % down * C::BQ, p0 = place / down * C::BP;
-    // no layout content sends a load out of the rows' buffers
-    int64_t start = __builtin_amdgcn_readfirstlane(a.seg.psum[expert]);
-    int64_t rows = __builtin_amdgcn_readfirstlane(a.seg.counts[expert]);
-    if (start < 0 || start >= a.seg.capacity || rows < 0) start = rows = 0;
-    if (rows > a.seg.capacity - start) rows = a.seg.capacity - start;
-    const uint32_t lds = lds_address(shared);
-    typename C::Sums sums;
-    ColsOperand<C::BQ, C::kThreads, false> q;
-    ColsOperand<C::BP, C::kThreads, GATHER> p;
-    q.init(static_cast<const char *>(a.g) + start * a.n * 2, 2 * static_cast<int64_t>(a.n), q0, a.n);
-    p.init(static_cast<const char *>(a.x) + (GATHER ? 0 : start * a.k * 2),
-           2 * static_cast<int64_t>(a.k), p0, a.k);
-    if (GATHER) p.gather(a.seg.src_meta + start, a.seg.num_topk, a.seg.num_tokens);
-    tile_product<C, true>(q, p, static_cast<int>(rows), C::BQ, lds, sums);
-    const int64_t base = static_cast<int64_t>(expert) * a.n;
+struct GradWeightTiles {
+    static constexpr int TQ = C::TQ, TP = C::TP;
+    static constexpr int kStores = TQ * TP / (F32 ? 1 : 2);
+    static_assert(TP % 2 == 0, "8 outputs a lane");
+    struct At : Job {
+        int expert, q0, p0;
+        int start;
+    };
+    typedef ColsOperand<C::BQ, C::kThreads, false, false> Q;
+    typedef ColsOperand<C::BP, C::kThreads, GATHER, true> P;
+    const GradWeightArgs &a;
+    const int down, across, wq, wp;
+    int64_t id, all, share;
+    int expert, start, rows;     // the expert that was looked up last
+
+    __device__ explicit GradWeightTiles(const GradWeightArgs &args)
+        : a(args), down((args.n + C::BQ - 1) / C::BQ), across((args.k + C::BP - 1) / C::BP),
+          wq(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / C::WP),
+          wp(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::WP), id(blockIdx.x),
+          expert(-1), start(0), rows(0) {
+        const uint32_t bits = static_cast<uint32_t>(a.seg.scalars[EP_SCALAR_ERROR_BITS]);
+        all = bits & EP_ERRBIT_FATAL ? 0
+                                     : static_cast<int64_t>(a.seg.num_experts) * down * across;
+        all = uniform(all);
+        share = (all + 7) / 8;
+    }
+    // Tiles without rows are zeros, and are written here.
+    EP_INLINE __device__ bool fetch(At &at) {
+        for (;; id += gridDim.x) {
+            if ((id >> 3) >= share) return false;
+            const int64_t tile = (id & 7) * share + (id >> 3);
+            if (tile >= all) continue;
+            at.expert = static_cast<int>(tile / (down * across));
+            const int place = static_cast<int>(tile % (down * across));
+            // strips of 6 tiles of Q, tiles of P along them: the 32 that are under way on an XCD have
+            // 12 operands between them, which its L2 holds (512 rows an expert, 4096 x 7168 and
+            // 7168 x 2048: 2.25 and 1.04 ms with strips of all tiles, 2.21 and 1.03 with 8, 2.13 and
+            // 1.02 with 6, 2.14 and 1.07 with 4)
+            constexpr int kStrip = 6;
+            const int strip = place / (kStrip * across), in = place % (kStrip * across);
+            const int left = down - strip * kStrip, high = left < kStrip ? left : kStrip;
+            at.q0 = (strip * kStrip + in % high) * C::BQ;
+            at.p0 = in / high * C::BP;
+            if (at.expert != expert) {
+                expert = at.expert;
+                // no layout content sends a load out of the rows' buffers
+                start = __builtin_amdgcn_readfirstlane(a.seg.psum[expert]);
+                rows = __builtin_amdgcn_readfirstlane(a.seg.counts[expert]);
+                if (start < 0 || start >= a.seg.capacity || rows < 0) start = rows = 0;
+                if (rows > a.seg.capacity - start) rows = static_cast<int>(a.seg.capacity - start);
+            }
+            at.start = start;
+            at.channels = rows;
+            if (rows > 0) {
+                id += gridDim.x;
+                return true;
+            }
+            typename C::Sums none;
 #pragma unroll
-    for (int t = 0; t < C::TQ; ++t) {
-        const int j = q0 + (t * C::WQ + wq) * M + lane % M;
-        if (j >= a.n) continue;
+            for (int t = 0; t < TQ; ++t)
 #pragma unroll
-        for (int u = 0; u < C::TP * kGroups; ++u) {
-            const int c = p0 + (wp * C::TP + u / kGroups) * M + u % kGroups * 8 + 4 * part;
-            if (c >= a.k) continue;
-            f32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = sums.v[t][u / kGroups][u % kGroups * 4 + i];
-            const int64_t to = (base + j) * a.k + c;
-            if (F32)
-                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to) = v;
-            else
-                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + to) =
-                    u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+                for (int u = 0; u < TP; ++u) none.v[t][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            finish(at, none);
         }
     }
+    EP_INLINE __device__ void start_q(Q &q, const At &at) {
+        q.init(static_cast<const char *>(a.g) + static_cast<int64_t>(at.start) * a.n * 2,
+               2 * static_cast<int64_t>(a.n), at.q0, a.n);
+    }
+    EP_INLINE __device__ void start_p(P &p, const At &at) {
+        p.init(static_cast<const char *>(a.x) +
+                   (GATHER ? 0 : static_cast<int64_t>(at.start) * a.k * 2),
+               2 * static_cast<int64_t>(a.k), at.p0, a.k);
+        if (GATHER) p.gather(a.seg.src_meta + at.start, a.seg.num_topk, a.seg.num_tokens);
+    }
+    EP_INLINE __device__ bool finish(const At &at, const typename C::Sums &sums) {
+        const int lane = thread_here() & 63;
+        const int c0 = at.p0 + wp * 16 * TP + (lane >> 4) * 4 * TP;      // the lane's first column
+#pragma unroll
+        for (int t = 0; t < TQ; ++t) {
+            const int j = at.q0 + (t * C::WQ + wq) * 16 + (lane & 15);
+            if (j >= a.n) continue;
+            const int64_t to = (static_cast<int64_t>(at.expert) * a.n + j) * a.k + c0;
+#pragma unroll
+            for (int u = 0; u < TP; u += 2) {
+                if (c0 + 4 * u >= a.k) continue;
+                const f32x4 v = sums.v[t][u], w = sums.v[t][u + 1];
+                if (F32) {
+                    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to + 4 * u);
+                    o[0] = v;
+                    o[1] = w;
+                } else {
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + to + 4 * u) =
+                        u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(w[0], w[1]),
+                              pack2(w[2], w[3])};
+                }
+            }
+        }
+        return at.q0 + C::BQ <= a.n && at.p0 + C::BP <= a.k;
+    }
+};
+
+template <typename C, bool GATHER, bool F32>
+__global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(
+    const GradWeightArgs a) {
+    extern __shared__ u32x4 shared[];
+    GradWeightTiles<C, GATHER, F32> tiles(a);
+    tile_stream<C>(tiles, lds_address(shared));
 }
 
 // The row weights' gradients from the tiles' sums, in the tiles' order.  One thread a slot.
@@ -361,8 +411,9 @@ hipError_t allow_lds(K kernel, int bytes) {
 
 constexpr int64_t kMostBlocks = int64_t(1) << 22;    // of a launch; a multiple of 8
 
-template <typename C, typename K, typename A>
-hipError_t launch_tiles(K kernel, const A &a, int64_t tiles, hipStream_t stream) {
+// A block for every tile.
+template <typename C, typename K>
+hipError_t launch_tiles(K kernel, const ExpertArgs &a, int64_t tiles, hipStream_t stream) {
     hipError_t e = allow_lds(kernel, C::kLds);
     if (e != hipSuccess) return e;
     const int64_t blocks = (tiles + 7) / 8 * 8;
@@ -373,6 +424,16 @@ hipError_t launch_tiles(K kernel, const A &a, int64_t tiles, hipStream_t stream)
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+// A block for every compute unit, which walks the tiles.
+template <typename C, typename K>
+hipError_t launch_stream(K kernel, const GradWeightArgs &a, int64_t tiles, hipStream_t stream) {
+    const hipError_t e = allow_lds(kernel, C::kLds);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = (persistent_grid(tiles, 1) + 7) / 8 * 8;
+    kernel<<<static_cast<uint32_t>(blocks), C::kThreads, C::kLds, stream>>>(a);
+    return hipGetLastError();
 }
 
 int64_t slots_of(const Segments &s) { return static_cast<int64_t>(s.num_tokens) * s.num_topk; }
@@ -394,22 +455,21 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream) {
     return launch_tiles<C>(expert_kernel<C, OUT, COLS, false>, a, tiles, stream);
 }
 
-template <template <int> class T, int OUT, bool COLS>
+template <typename T, int OUT, bool COLS>
 hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream) {
     const int64_t slots = slots_of(a.seg), experts = a.seg.num_experts;
-    if (slots > 64 * experts) return launch_expert<Tile<T<16>, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
-    if (slots > 16 * experts) return launch_expert<Tile<T<16>, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
+    if (slots > 64 * experts) return launch_expert<Tile<T, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
+    if (slots > 16 * experts) return launch_expert<Tile<T, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
     if constexpr (COLS)
-        return launch_expert<Tile<T<16>, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
     else
-        return launch_expert<Tile<T<16>, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
+        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
 }
 
 }  // namespace
 
-constexpr int kGateGradColumns = 256;
-
-int gate_grad_tiles(int32_t inter) { return (inter + kGateGradColumns - 1) / kGateGradColumns; }
+// A wave's sums are of 64 columns.
+int gate_grad_tiles(int32_t inter) { return (inter + 255) / 256 * 4; }
 
 hipError_t launch_expert_i8(const ExpertArgs &a, bool gated, hipStream_t stream) {
     return gated ? choose_expert<Int8, kGated, false>(a, stream)
@@ -426,7 +486,7 @@ hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t stream) {
 
 hipError_t launch_expert_gate_grad(const ExpertArgs &a, float *grad_row_weights, const int32_t *dst,
                                    hipStream_t stream) {
-    hipError_t e = launch_expert<Tile<Bf16<16>, 256, kGateGradColumns, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
+    hipError_t e = launch_expert<Tile<Bf16, 256, 256, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
     if (e != hipSuccess || !grad_row_weights) return e;
     const int64_t slots = slots_of(a.seg), blocks = (slots + 255) / 256;
     row_sums_kernel<<<static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
@@ -440,14 +500,14 @@ hipError_t launch_expert_grad_rows(const ExpertArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_expert_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
-    typedef Tile<Bf16<16>, 256, 256, 2, 4, 2, 3> C;
+    typedef Tile<Bf16, 256, 256, 2, 4, 2, 3> C;
     const int64_t tiles = static_cast<int64_t>(a.seg.num_experts) * ((a.n + C::BQ - 1) / C::BQ) *
                           ((a.k + C::BP - 1) / C::BP);
     if (a.f32)
-        return a.token_rows ? launch_tiles<C>(grad_weight_kernel<C, true, true>, a, tiles, stream)
-                            : launch_tiles<C>(grad_weight_kernel<C, false, true>, a, tiles, stream);
-    return a.token_rows ? launch_tiles<C>(grad_weight_kernel<C, true, false>, a, tiles, stream)
-                        : launch_tiles<C>(grad_weight_kernel<C, false, false>, a, tiles, stream);
+        return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, true>, a, tiles, stream)
+                            : launch_stream<C>(grad_weight_kernel<C, false, true>, a, tiles, stream);
+    return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, false>, a, tiles, stream)
+                        : launch_stream<C>(grad_weight_kernel<C, false, false>, a, tiles, stream);
 }
 
 }  // namespace ep

@@ -50,30 +50,32 @@ __device__ inline u32x2 codes8(const u32x4 v, float s, float y) {
     return u32x2{pack(0), pack(4)};
 }
 
-// One row by W waves, V vectors of 8 channels a lane in registers.
+// One row by W waves of a block of four, V vectors of 8 channels a lane in registers.
 template <int W, int V>
-__global__ __launch_bounds__(64 * W) void quant_i8_kernel(const QuantI8Args a, int64_t first) {
-    __shared__ uint32_t tops[W];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int vecs = a.channels / 8;
-    int64_t row = first + blockIdx.x;
-    if (a.dst) {
+__global__ __launch_bounds__(256) void quant_i8_kernel(const QuantI8Args a, int64_t first) {
+    __shared__ uint32_t tops[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int vecs = a.channels / 8, me = wave % W * 64 + lane;
+    int64_t row = first + blockIdx.x * static_cast<int64_t>(4 / W) + wave / W;
+    bool here = row < a.num_rows;
+    if (a.dst && here) {
         const uint32_t bits = static_cast<uint32_t>(a.scalars[EP_SCALAR_ERROR_BITS]);
         row = a.dst[row];
-        if (row < 0 || row >= a.capacity || (bits & EP_ERRBIT_FATAL)) return;
+        here = row >= 0 && row < a.capacity && !(bits & EP_ERRBIT_FATAL);
     }
+    if (!here) return;                                       // W == 1, or the whole block
     const u32x4 *x = static_cast<const u32x4 *>(a.x) + row * vecs;
     u32x4 v[V];
     u16x2 m = u16x2{0, 0};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = i * 64 * W + threadIdx.x;
+        const int at = i * 64 * W + me;
         v[i] = at < vecs ? x[at] : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) m = larger(m, v[i]);
-    uint32_t top = static_cast<uint32_t>(m.x > m.y ? m.x : m.y) << 16;
-    top = wave_max(top);
+    uint32_t top = wave_max(static_cast<uint32_t>(m.x > m.y ? m.x : m.y) << 16);
     if (W > 1) {
         if (lane == 0) tops[wave] = top;
         __syncthreads();
@@ -87,18 +89,19 @@ __global__ __launch_bounds__(64 * W) void quant_i8_kernel(const QuantI8Args a, i
     u32x2 *q = static_cast<u32x2 *>(a.q) + row * vecs;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = i * 64 * W + threadIdx.x;
+        const int at = i * 64 * W + me;
         if (at < vecs) q[at] = fine ? codes8(v[i], s, y) : u32x2{0u, 0u};
     }
-    if (threadIdx.x == 0) a.scale[row] = fine ? s : __uint_as_float(0x7FC00000u);
+    if (me == 0) a.scale[row] = fine ? s : __uint_as_float(0x7FC00000u);
 }
 
 template <int W, int V>
 hipError_t launch_quant(const QuantI8Args &a, hipStream_t stream) {
-    constexpr int64_t kMost = int64_t(1) << 22;      // fewer than 2^32 threads a launch
+    constexpr int64_t kMost = int64_t(1) << 24;      // rows; fewer than 2^32 threads a launch
     for (int64_t r = 0; r < a.num_rows; r += kMost) {
         const int64_t n = a.num_rows - r < kMost ? a.num_rows - r : kMost;
-        quant_i8_kernel<W, V><<<static_cast<uint32_t>(n), 64 * W, 0, stream>>>(a, r);
+        const int64_t blocks = (n * W + 3) / 4;
+        quant_i8_kernel<W, V><<<static_cast<uint32_t>(blocks), 256, 0, stream>>>(a, r);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -107,12 +110,19 @@ hipError_t launch_quant(const QuantI8Args &a, hipStream_t stream) {
 
 }  // namespace
 
+// Many rows: a wave each, which waits for no other one (32768 rows of 2048: 45 us by four waves).
+// Few: four waves, as a row's latency is what counts.
 hipError_t launch_quantize_i8(const QuantI8Args &a, hipStream_t stream) {
     const int vecs = a.channels / 8;
+    const bool many = a.num_rows >= 2048;
+    if (vecs <= 64) return launch_quant<1, 1>(a, stream);
     if (vecs <= 128) return launch_quant<1, 2>(a, stream);
+    if (many && vecs <= 256) return launch_quant<1, 4>(a, stream);
+    if (many && vecs <= 512) return launch_quant<1, 8>(a, stream);
+    if (vecs <= 256) return launch_quant<4, 1>(a, stream);
     if (vecs <= 512) return launch_quant<4, 2>(a, stream);
     if (vecs <= 1024) return launch_quant<4, 4>(a, stream);
-    return launch_quant<8, 8>(a, stream);
+    return launch_quant<4, 16>(a, stream);
 }
 
 }  // namespace ep

@@ -7,7 +7,7 @@
 // expert's rows).  A chunk is 128 bytes of channels: 64 in bf16, 128 in int8.
 //
 // Chunks go from memory straight to LDS (global_load_lds, 16 bytes a lane), `S` of them in a
-// ring.  Rows operands: an LDS row is 128 bytes, its 16-byte units permuted by the row's number, so
+// ring.  Rows operands: an LDS row is 128 bytes, its 16-byte units permuted by u ^ (row % 8), so
 // that the rows which LDS serves together are in different banks.  Cols operands: an LDS
 // row is one channel's BQ or BP values; ds_read_b64_tr_b16 hands each lane the four channels of
 // its own column.  The permutations are made by the addresses that the lanes load from, as the
@@ -24,32 +24,39 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 #define EP_LDS __attribute__((address_space(3)))
+#define EP_INLINE __attribute__((always_inline))
 
-// Matrix instructions of M x M outputs.  Lane l holds p = l % M of the first operand, q = l % M
-// of the second, 16 bytes of channels at 16 (l / M) of both, and four consecutive outputs in
-// each of `groups` groups: p = 4 (64 / M) g + 4 (l / M) + i of q = l % M.
-template <int M_>
+// 16 x 16 outputs of 64 bytes of channels: lane l holds p = l % 16 of the first operand, q =
+// l % 16 of the second, the 16 bytes of channels at 16 (l / 16) of both, and the outputs
+// p = 4 (l / 16) + i of q = l % 16.  (Instructions of 32 x 32 outputs: 1.62 ms in place of 1.55 for
+// 64 experts of 512 rows, 7168 to 4096 channels, at 1.56 GHz in place of 1.62: the
+// card's power is what bounds a product of these sizes; on zeros both run a sixth faster.)
 struct Bf16 {
-    static constexpr int M = M_, kBytes = 2, kGroups = M * M / 256;
-    typedef float Acc __attribute__((ext_vector_type(4 * kGroups)));
+    typedef f32x4 Acc;
+    static constexpr int kBytes = 2;
     static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
-        const bf16x8 a = __builtin_bit_cast(bf16x8, p), b = __builtin_bit_cast(bf16x8, q);
-        if constexpr (M == 16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-        else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p),
+                                                       __builtin_bit_cast(bf16x8, q), c, 0, 0, 0);
     }
 };
 
 // Sums of 32768 products of codes stay below 2^30: nothing is rounded.
-template <int M_>
 struct Int8 {
-    static constexpr int M = M_, kBytes = 1, kGroups = M * M / 256;
-    typedef int32_t Acc __attribute__((ext_vector_type(4 * kGroups)));
+    typedef i32x4 Acc;
+    static constexpr int kBytes = 1;
     static __device__ inline Acc mma(u32x4 p, u32x4 q, Acc c) {
-        const i32x4 a = __builtin_bit_cast(i32x4, p), b = __builtin_bit_cast(i32x4, q);
-        if constexpr (M == 16) return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-        else return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, p),
+                                                     __builtin_bit_cast(i32x4, q), c, 0, 0, 0);
     }
 };
+
+// The thread's number, as if it were new: what is worked out from it for one tile is not kept in
+// registers over all of them.
+__device__ inline int thread_here() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
 
 // A value that is the same in every lane, in a scalar register.
 __device__ inline int64_t uniform(int64_t v) {
@@ -93,9 +100,8 @@ __device__ inline u32x4 read_lds(uint32_t at) {
     return *reinterpret_cast<EP_LDS u32x4 *>(static_cast<uintptr_t>(at));
 }
 
-__device__ inline void zero_lds(uint32_t at) {
-    *reinterpret_cast<EP_LDS u32x4 *>(static_cast<uintptr_t>(at)) = u32x4{0u, 0u, 0u, 0u};
-}
+// What lanes load that have nothing to load: every chunk is then the same number of loads.
+static __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
 // Where the rows of a token-rows call lie: the slot's token, inside the batch whatever the
 // layout holds (a call captured for fewer tokens than a later layout has reads the last of
@@ -119,22 +125,22 @@ struct RowsOperand {
     uint32_t off[GATHER ? 1 : kLoads];
     const char *from[GATHER ? kLoads : 1];
     uint32_t to;             // of the wave's first load in a stage
-    int unit;                // of 16 bytes in the chunk, the same in every load
     bool mine;
 
-    static __device__ int row(int i) { return i * (Threads / 8) + threadIdx.x / 8; }
-    static __device__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
+    // The thread's 16 bytes in the chunk, the same in every load.
+    static __device__ int unit(int thread) { return (thread & 7) ^ ((thread >> 3) & 7); }
 
     template <typename RowOf>
     __device__ void init(const void *b, RowOf row_of) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         base = uniform(b);
-        unit = (threadIdx.x & 7) ^ swizzle(threadIdx.x >> 3);
+        const int thread = thread_here();
         to = wave * 1024;
         mine = !kPart || wave * 1024 < kBytes;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int64_t at = row_of(mine ? row(i) : 0) + unit * 16;
+            const int64_t at =
+                row_of(mine ? i * (Threads / 8) + thread / 8 : 0) + unit(thread) * 16;
             if (GATHER) from[i] = base + at;
             else off[i] = static_cast<uint32_t>(at);
         }
@@ -152,31 +158,27 @@ struct RowsOperand {
     __device__ void advance() {
         if (!GATHER) base += 128;
     }
-    // The last chunk, of which T has `channels`; what is missing is zeros.
-    template <typename T, int N>
-    __device__ void load_end(uint32_t stage, int channels) {
+    // Load i of a chunk of which T has `channels`; what is missing is zeros.
+    template <typename T>
+    __device__ void load_end(uint32_t stage, int i, int channels) {
         if (kPart && !mine) return;
-        const bool in = unit * 16 < channels * T::kBytes;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t at = stage + to + i * Threads * 16;
-            if (!in) zero_lds(at + (threadIdx.x & 63) * 16);
-            else if (GATHER) load_lds(at, from[i]);
-            else load_lds(at, base, off[i]);
-        }
+        const char *at = GATHER ? from[GATHER ? i : 0] : base + off[GATHER ? 0 : i];
+        const bool in = unit(thread_here()) * 16 < channels * T::kBytes;
+        load_lds(stage + to + i * Threads * 16, in ? at : reinterpret_cast<const char *>(&kZeros));
     }
-    // The wave's operand of a matrix instruction: rows M t .., the k-th 1024 / M bytes of channels.
-    template <int M>
-    static __device__ u32x4 fragment(uint32_t stage, int t, int k) {
-        const int lane = threadIdx.x & 63;
-        return read_lds(stage + (M * t + lane % M) * 128 +
-                        (((k * (64 / M) + lane / M) ^ swizzle(M * t + lane % M)) << 4));
+    // The wave's operand of a matrix instruction: rows 16 t .., channels of 64 bytes `half`.
+    template <int TP>
+    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
+        const int lane = threadIdx.x & 63, r = 16 * t + (lane & 15);
+        return read_lds(stage + r * 128 + (((half * 4 + (lane >> 4)) ^ (r & 7)) << 4));
     }
 };
 
-// An operand of C columns, channel by channel, in bf16.  `from(i)` gives the byte offset of the
-// thread's 16 bytes in load i from `base`, or its address (GATHER).
-template <int C, int Threads, bool GATHER>
+// An operand of C columns, channel by channel, in bf16.  CONSECUTIVE: the columns of a wave's TP
+// matrix instructions are dealt out so that a lane's sums lie side by side, part l / 16 of the
+// wave's columns having 4 in each instruction: the transposing read takes any four columns
+// that lie together.
+template <int C, int Threads, bool GATHER, bool CONSECUTIVE>
 struct ColsOperand {
     static constexpr int kRow = 2 * C;                       // bytes of a channel
     static constexpr int kBytes = 64 * kRow;
@@ -185,26 +187,29 @@ struct ColsOperand {
     static_assert(kBytes % (Threads * 16) == 0 && C >= 128, "whole loads");
     const char *base;
     int64_t pitch;           // bytes from a channel to the next
-    uint32_t col;            // byte offset of the thread's unit in its channel, as loaded
     uint32_t off[kLoads];
     const int32_t *src_meta; // GATHER: of the segment's rows
     int topk, tokens;
     uint32_t to;
 
-    static __device__ int channel(int i) { return (i * Threads + threadIdx.x) / (kRow / 16); }
-    // Units of 32 bytes are permuted by these bits of the channel: a read takes 32 bytes of
-    // four consecutive channels in each row of 16 lanes, rows of lanes being 8 channels apart.
-    static __device__ int swizzle(int ch) { return (ch & 3) | ((ch >> 1) & 4); }
+    static __device__ int channel(int i, int thread) { return (i * Threads + thread) / (kRow / 16); }
+    // Units of 16 bytes are permuted by these bits of the channel.  A read takes four times
+    // 8 bytes of four consecutive channels in each row of 16 lanes: 32 bytes of a channel, or
+    // CONSECUTIVE four pieces 32 bytes apart.
+    static __device__ int swizzle(int ch) {
+        return CONSECUTIVE ? (ch & 1) | ((ch << 2) & 8) : ((ch & 3) | ((ch >> 1) & 4)) << 1;
+    }
 
     // Columns `first` .. of `cols` (in a row of `pitch` bytes) from channel 0 at `b`.
     __device__ void init(const void *b, int64_t row_pitch, int first, int cols) {
         base = uniform(b);
         pitch = uniform(row_pitch);
         to = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+        const int thread = thread_here();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int ch = channel(i);
-            const int unit = (threadIdx.x % (kRow / 16)) ^ (swizzle(ch) << 1);
+            const int ch = channel(i, thread);
+            const int unit = (thread % (kRow / 16)) ^ swizzle(ch);
             int c = first + unit * 8;
             if (c >= cols) c = cols - 8;                     // computed on, and not stored
             off[i] = (GATHER ? 0u : static_cast<uint32_t>(ch * pitch)) + 2u * c;
@@ -216,37 +221,39 @@ struct ColsOperand {
         tokens = t;
     }
     // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
-    __device__ void load(uint32_t stage, int i) { load_one(stage + to + i * Threads * 16, i); }
+    __device__ void load(uint32_t stage, int i) {
+        if (GATHER) load_lds(stage + to + i * Threads * 16, address(i));
+        else load_lds(stage + to + i * Threads * 16, uniform(base), off[i]);
+    }
     __device__ void advance() {
         if (GATHER) src_meta += 64;
         else base += 64 * pitch;
     }
-    // The last chunk, of which `channels` are there; what is missing is zeros.
-    template <typename T, int N>
-    __device__ void load_end(uint32_t stage, int channels) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t at = stage + to + i * Threads * 16;
-            if (channel(i) < channels) load_one(at, i);
-            else zero_lds(at + (threadIdx.x & 63) * 16);
-        }
+    // Load i of a chunk of which `channels` are there; what is missing is zeros.
+    template <typename T>
+    __device__ void load_end(uint32_t stage, int i, int channels) {
+        const char *at = reinterpret_cast<const char *>(&kZeros);
+        if (channel(i, thread_here()) < channels) at = address(i);
+        load_lds(stage + to + i * Threads * 16, at);
     }
-    __device__ void load_one(uint32_t at, int i) {
-        if (GATHER)
-            load_lds(at, base + token_of(src_meta, channel(i), topk, tokens) * pitch + off[i]);
-        else
-            load_lds(at, base, off[i]);
+    __device__ const char *address(int i) {
+        const char *b = base;
+        return GATHER ? b + token_of(src_meta, channel(i, thread_here()), topk, tokens) * pitch +
+                            off[i]
+                      : b + off[i];
     }
-    template <int M>
-    static __device__ u32x4 fragment(uint32_t stage, int t, int k) {
+    template <int TP>
+    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
         const int lane = threadIdx.x & 63, j = lane & 15;
-        const int ch = k * (512 / M) + lane / M * 8 + (j >> 2);
-        const int unit = t * (M / 16) + lane % M / 16;       // 16 columns
+        const int ch = half * 32 + (lane >> 4) * 8 + (j >> 2);
+        // four columns, of 8 bytes
+        const int piece = CONSECUTIVE ? t / TP * 4 * TP + (j & 3) * TP + t % TP : 4 * t + (j & 3);
         u32x4 v;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c = ch + 4 * i;
-            const uint32_t at = stage + c * kRow + ((unit ^ swizzle(c)) << 5) + (j & 3) * 8;
+            const uint32_t at =
+                stage + c * kRow + (((piece >> 1) ^ swizzle(c)) << 4) + (piece & 1) * 8;
             const u32x2 r = __builtin_bit_cast(
                 u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                            reinterpret_cast<EP_LDS s16x4 *>(static_cast<uintptr_t>(at))));
@@ -270,9 +277,9 @@ struct Tile {
     typedef T Type;
     static constexpr int BQ = BQ_, BP = BP_, WQ = WQ_, WP = WP_, SQ = SQ_, SP = SP_;
     static_assert(SQ >= 2 && (SP == SQ || SP == SQ + 1), "what the waits count on");
-    static constexpr int M = T::M, TQ = BQ / M / WQ, TP = BP / M / WP;
+    static constexpr int TQ = BQ / 16 / WQ, TP = BP / 16 / WP;
     static constexpr int kThreads = 64 * WQ * WP;
-    static constexpr int kBlocks = kThreads >= 512 || TQ * TP > 32 ? 1 : 512 / kThreads;
+    static constexpr int kBlocks = kThreads >= 512 ? 1 : 512 / kThreads;
     typedef typename T::Acc Acc;
     struct Sums {
         Acc v[TQ][TP];
@@ -298,7 +305,7 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
     constexpr int TQ = C::TQ, TP = C::TP, kPerChunk = 128 / T::kBytes;
     constexpr int NQ = Q::kLoads, NP = P::kLoads;
     static_assert(!P::kPart, "every wave loads of P");
-    const int active = (rows + C::M * C::WQ - 1) / (C::M * C::WQ);       // row tiles a wave
+    const int active = (rows + 16 * C::WQ - 1) / (16 * C::WQ);       // row tiles a wave
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wq = wave / C::WP, wp = wave % C::WP;
     const int chunks = (channels + kPerChunk - 1) / kPerChunk, whole = channels / kPerChunk;
@@ -315,7 +322,9 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
             for (int i = 0; i < N; ++i) o.load(stage, i);
             o.advance();
         } else if (chunk < chunks) {
-            o.template load_end<T, N>(stage, channels - chunk * kPerChunk);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o.template load_end<T>(stage, i, channels - chunk * kPerChunk);
         }
     };
     // Until chunk c has come.  Behind its loads SQ - 2 chunks of Q and SP - 2 of P set out, in the
@@ -327,17 +336,12 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
         else if (Q::kPart && !q.mine) wait_loads<BP * NP>();
         else wait_loads<BQ * NQ + BP * NP>();
     };
-    constexpr int K = C::M / 16;                 // matrix instructions of 64 bytes of channels
     struct Half {
-        u32x4 q[TQ][K], p[TP][K];
+        u32x4 q[TQ], p[TP];
     };
     auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) {
-        const int k = i % K, t = i / K;
-        if (t < TP)
-            f.p[t][k] = P::template fragment<C::M>(stage_p, wp * TP + t, half * K + k);
-        else
-            f.q[t - TP][k] =
-                Q::template fragment<C::M>(stage_q, (t - TP) * C::WQ + wq, half * K + k);
+        if (i < TP) f.p[i] = P::template fragment<TP>(stage_p, wp * TP + i, half);
+        else f.q[i - TP] = Q::template fragment<TP>(stage_q, (i - TP) * C::WQ + wq, half);
     };
     // Multiplies `now`, a row tile at a time, while `then` is read and, with LOAD, the N loads of
     // a chunk set out.  Issued all at once the loads take the address unit 16 cycles each, in
@@ -359,15 +363,12 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
                 if (a == kEarly - 1) o.advance();
             }
 #pragma unroll
-            for (int i = 0; i < (TP + TQ) * K; ++i)
-                if (ALL ? i * TQ / ((TP + TQ) * K) == a
-                        : i < TP * K ? i * kEarly / (TP * K) == a : i / K - TP == a)
+            for (int i = 0; i < TP + TQ; ++i)
+                if (ALL ? i * TQ / (TP + TQ) == a
+                        : i < TP ? i * kEarly / TP == a : i - TP == a)
                     read(then, stage_q, stage_p, half, i);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int b = 0; b < TP; ++b)
-                    sums.v[a][b] = T::mma(now.p[b][k], now.q[a][k], sums.v[a][b]);
+            for (int b = 0; b < TP; ++b) sums.v[a][b] = T::mma(now.p[b], now.q[a], sums.v[a][b]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -383,7 +384,7 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
     uint32_t at_q = ring_q, at_p = ring_p, free_p = 0;
     Half first, second;
 #pragma unroll
-    for (int i = 0; i < (TP + TQ) * K; ++i) read(first, at_q, at_p, 0, i);
+    for (int i = 0; i < TP + TQ; ++i) read(first, at_q, at_p, 0, i);
     // `steady`: the chunks that set out are whole ones
     auto chunk = [&](int c, auto steady) {
         constexpr bool kSteady = decltype(steady)::value != 0;
@@ -404,6 +405,199 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
     chunk(c++, Int<0>());
     for (; c + C::SQ < whole && c + C::SP <= whole; ++c) chunk(c, Int<1>());
     for (; c < chunks; ++c) chunk(c, Int<0>());
+}
+
+// A tile to be made: what its operands lie at is the source's business.
+struct Job {
+    int channels;            // that are summed
+};
+
+// Makes one tile after the other.  A source has
+//   bool fetch(At &)               the block's next tile, if there is one (never one without channels)
+//   void start_q(Q &, const At &)  sets an operand to a tile's first chunk
+//   void start_p(P &, const At &)
+//   bool finish(const At &, Sums &) stores a tile; whether every wave issued exactly kStores
+//                                  store instructions
+// with At derived from Job.  The chunks of all tiles are one stream: the next tile's first ones are
+// on their way while a tile's last ones are multiplied and its sums stored.
+// Otherwise as tile_product.
+template <typename C, typename S>
+__device__ inline void tile_stream(S &src, uint32_t lds) {
+    typedef typename C::Type T;
+    typedef typename S::Q Q;
+    typedef typename S::P P;
+    typedef typename S::At At;
+    constexpr int TQ = C::TQ, TP = C::TP, kPerChunk = 128 / T::kBytes;
+    constexpr int NQ = Q::kLoads, NP = P::kLoads;
+    constexpr int BQ = C::SQ - 2, BP = C::SP - 2;
+    static_assert(!Q::kPart && !P::kPart, "every wave loads");
+    static_assert(BQ * NQ + BP * NP + S::kStores < 64, "what a wave can count");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wq = wave / C::WP, wp = wave % C::WP;
+    const uint32_t ring_q = lds, ring_p = lds + C::kRingQ, end = lds + C::kLds;
+    At now, then;
+    auto fetch = [&](At &at) EP_INLINE {
+        const int some = __builtin_amdgcn_readfirstlane(src.fetch(at) ? 1 : 0);
+        at.channels = __builtin_amdgcn_readfirstlane(at.channels);
+        return some != 0;
+    };
+    if (!fetch(now)) return;
+    bool more = fetch(then);
+    Q q;
+    P p;
+    src.start_q(q, now);
+    src.start_p(p, now);
+    // What is loaded next: so many channels are left of the tile that the operand is at, which
+    // is `then` where `ahead`; `count` chunks have set out, the next goes to `room`.
+    struct Loader {
+        int left, count;
+        bool ahead;
+        uint32_t room;
+    };
+    Loader lq = {now.channels, 0, false, ring_q}, lp = {now.channels, 0, false, ring_p};
+    // The channels of the next chunk, or 0 where there is none.
+    auto next_q = [&]() EP_INLINE {
+        if (lq.left <= 0 && !lq.ahead && more) {
+            src.start_q(q, then);
+            lq.left = then.channels;
+            lq.ahead = true;
+        }
+        return lq.left;
+    };
+    auto next_p = [&]() EP_INLINE {
+        if (lp.left <= 0 && !lp.ahead && more) {
+            src.start_p(p, then);
+            lp.left = then.channels;
+            lp.ahead = true;
+        }
+        return lp.left;
+    };
+    // One of its loads (the branches are the same in all lanes).
+    auto load_q = [&](int left, int i) EP_INLINE {
+        if (left >= kPerChunk) q.load(lq.room, i);
+        else if (left > 0) q.template load_end<T>(lq.room, i, left);
+    };
+    auto load_p = [&](int left, int i) EP_INLINE {
+        if (left >= kPerChunk) p.load(lp.room, i);
+        else if (left > 0) p.template load_end<T>(lp.room, i, left);
+    };
+    // After its last load.
+    auto loaded_q = [&](int left) EP_INLINE {
+        if (left <= 0) return;
+        q.advance();
+        lq.left -= kPerChunk;
+        ++lq.count;
+        lq.room = lq.room + C::kStageQ == ring_p ? ring_q : lq.room + C::kStageQ;
+    };
+    auto loaded_p = [&](int left) EP_INLINE {
+        if (left <= 0) return;
+        p.advance();
+        lp.left -= kPerChunk;
+        ++lp.count;
+        lp.room = lp.room + C::kStageP == end ? ring_p : lp.room + C::kStageP;
+    };
+    // Chunks until so many have set out.
+    auto fill_q = [&](int count) EP_INLINE {
+        bool some = false;
+#pragma clang loop unroll(disable)
+        while (lq.count < count) {
+            const int left = next_q();
+            if (left <= 0) break;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) load_q(left, i);
+            loaded_q(left);
+            some = true;
+        }
+        return some;
+    };
+    auto fill_p = [&](int count) EP_INLINE {
+        bool some = false;
+#pragma clang loop unroll(disable)
+        while (lp.count < count) {
+            const int left = next_p();
+            if (left <= 0) break;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) load_p(left, i);
+            loaded_p(left);
+            some = true;
+        }
+        return some;
+    };
+    struct Half {
+        u32x4 q[TQ], p[TP];
+    };
+    auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) EP_INLINE {
+        if (i < TP) f.p[i] = P::template fragment<TP>(stage_p, wp * TP + i, half);
+        else f.q[i - TP] = Q::template fragment<TP>(stage_q, (i - TP) * C::WQ + wq, half);
+    };
+    typename C::Sums sums;
+    // Multiplies `f`, a row tile at a time, while `b` is read and the N loads of a chunk set out.
+    auto step = [&](const Half &f, Half &b, uint32_t stage_q, uint32_t stage_p, int half, auto count,
+                    auto load) EP_INLINE {
+        constexpr int N = decltype(count)::value;
+        constexpr int kEarly = (TQ + 1) / 2;                 // row tiles in which loads set out
+#pragma unroll
+        for (int t = 0; t < TQ; ++t) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i * kEarly / N == t) load(i);
+#pragma unroll
+            for (int i = 0; i < TP + TQ; ++i)
+                if (i * TQ / (TP + TQ) == t) read(b, stage_q, stage_p, half, i);
+#pragma unroll
+            for (int u = 0; u < TP; ++u) sums.v[t][u] = T::mma(f.p[u], f.q[t], sums.v[t][u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    fill_p(C::SP);
+    fill_q(C::SQ);
+    wait_loads<0>();
+    block_barrier();
+    uint32_t at_q = ring_q, at_p = ring_p;
+    Half first, second;
+#pragma unroll
+    for (int i = 0; i < TP + TQ; ++i) read(first, at_q, at_p, 0, i);
+    int g = 0;                                   // chunks before this one
+    int stores = 0;
+    for (;;) {
+#pragma unroll
+        for (int t = 0; t < TQ; ++t)
+#pragma unroll
+            for (int u = 0; u < TP; ++u) {
+                sums.v[t][u] = typename C::Acc(0);
+                asm("" : "+v"(sums.v[t][u]));    // zeros like others: no first chunk of its own
+            }
+        const int last = g + (now.channels + kPerChunk - 1) / kPerChunk;
+#pragma clang loop unroll(disable)
+        for (; g < last; ++g) {
+            // the first chunk's were loaded above
+            const int left_p = lp.count < g + C::SP ? next_p() : 0;
+            step(first, second, at_q, at_p, 1, Int<NP>(), [&](int i) EP_INLINE { load_p(left_p, i); });
+            loaded_p(left_p);
+            // chunk g + 1 has come: BQ chunks of Q and BP of P may still be on their way, and
+            // what was stored since
+            const bool known = lq.count == g + C::SQ && lp.count == g + C::SP && stores >= 0;
+            if (!known) wait_loads<0>();
+            else if (stores > 0) wait_loads<BQ * NQ + BP * NP + S::kStores>();
+            else wait_loads<BQ * NQ + BP * NP>();
+            stores = 0;
+            block_barrier();
+            at_q = at_q + C::kStageQ == ring_p ? ring_q : at_q + C::kStageQ;
+            at_p = at_p + C::kStageP == end ? ring_p : at_p + C::kStageP;
+            // behind the last chunk nothing has come: what is read is not used
+            const int left_q = next_q();
+            step(second, first, at_q, at_p, 0, Int<NQ>(), [&](int i) EP_INLINE { load_q(left_q, i); });
+            loaded_q(left_q);
+        }
+        stores = src.finish(now, sums) ? S::kStores : -1;
+        if (!more) return;
+        now = then;                              // both operands have begun with it
+        lq.ahead = lp.ahead = false;
+        more = fetch(then);
+        // tiles of few chunks: what the loaders could not see before
+        if (fill_q(g + C::SQ)) stores = -1;
+        if (fill_p(g + C::SP - 1)) stores = -1;
+    }
 }
 
 }  // namespace ep

@@ -27,14 +27,23 @@ struct Place {
 // each other, row tiles fastest, so what is under way on an XCD at a time shares weights.
 __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int across, int lane) {
     const int experts = seg.num_experts;
+    int count = 0, upto = 0, start = 0;          // of the lane's expert; row tiles up to it
+    auto load = [&](int e0) {
+        const int e = e0 + lane;
+        count = e < experts ? seg.counts[e] : 0;
+        start = e < experts ? seg.psum[e] : 0;
+        if (count < 0) count = 0;
+        upto = (count + per - 1) / per;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int below = __shfl_up(upto, d);
+            if (lane >= d) upto += below;
+        }
+    };
     int64_t all = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
-        const int e = e0 + lane;
-        const int c = e < experts ? seg.counts[e] : 0;
-        int t = c > 0 ? (c + per - 1) / per : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) t += __shfl_xor(t, d);
-        all += __builtin_amdgcn_readfirstlane(t);
+        load(e0);
+        all += __builtin_amdgcn_readlane(upto, 63);
     }
     all *= across;
     const int64_t part = (all + 7) / 8, tile = (id & 7) * part + (id >> 3);
@@ -42,15 +51,7 @@ __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int 
     int pass = static_cast<int>(tile / across);
     int64_t before = 0;      // row tiles of the experts so far
     for (int e0 = 0; e0 < experts; e0 += 64) {
-        const int e = e0 + lane;
-        const int c = e < experts ? seg.counts[e] : 0;
-        const int mine = c > 0 ? (c + per - 1) / per : 0;
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int below = __shfl_up(upto, d);
-            if (lane >= d) upto += below;
-        }
+        if (experts > 64) load(e0);
         const int sum = __builtin_amdgcn_readlane(upto, 63);
         if (pass >= sum) {
             pass -= sum;
@@ -60,14 +61,13 @@ __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int 
         // the first lane whose sum is past the number
         const int l = __builtin_amdgcn_readfirstlane(
             __ffsll(static_cast<unsigned long long>(__ballot(upto > pass))) - 1);
-        const int tiles = __builtin_amdgcn_readlane(mine, l);
-        const int count = __builtin_amdgcn_readlane(c, l);
+        const int rows = __builtin_amdgcn_readlane(count, l), tiles = (rows + per - 1) / per;
         before += __builtin_amdgcn_readlane(upto, l) - tiles;
         const int at = static_cast<int>(tile - before * across);
-        const int size = ((count + tiles - 1) / tiles + 15) / 16 * 16;
+        const int size = ((rows + tiles - 1) / tiles + 15) / 16 * 16;
         const int first = at % tiles * size;
-        return {e0 + l, seg.psum[e0 + l] + first, count - first < size ? count - first : size,
-                at / tiles};
+        return {e0 + l, __builtin_amdgcn_readlane(start, l) + first,
+                rows - first < size ? rows - first : size, at / tiles};
     }
     return {-1, 0, 0, 0};
 }
@@ -110,16 +110,16 @@ enum Out { kPlain, kGated, kGateGrad };
 // The sums lie in the lanes as four outputs of one row from each matrix instruction.  Which weight
 // goes to which place of the tile is free: a lane's outputs are made consecutive, and it stores 8 of
 // them (16 bytes) at a time.
-template <typename C, int OUT, bool COLS, bool GATHER>
+template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 struct ExpertTile {
     static constexpr bool I8 = C::Type::kBytes == 1;
     static constexpr int TQ = C::TQ, TP = C::TP;
     static constexpr int G = OUT == kGated ? TP / 2 : TP;    // matrix instructions of outputs
     static constexpr int BP = 16 * C::WP * G;                // outputs of a tile
     static constexpr int U = 4 * G < 8 ? 4 * G : 8;          // stored at a time
-    typedef RowsOperand<C::BQ, C::kThreads, GATHER> Q;
-    typedef std::conditional_t<COLS, ColsOperand<C::BP, C::kThreads, false, true>,
-                               RowsOperand<C::BP, C::kThreads, false>> P;
+    typedef RowsOperand<C::BQ, C::kThreads, GATHER, false> Q;
+    typedef std::conditional_t<COLS, ColsOperand<C::BP, C::kThreads, false, true, ONCE>,
+                               RowsOperand<C::BP, C::kThreads, false, ONCE>> P;
     const ExpertArgs &a;
     const Place &at;
 
@@ -253,10 +253,10 @@ struct ExpertTile {
     }
 };
 
-template <typename C, int OUT, bool COLS, bool GATHER>
+template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const ExpertArgs a,
                                                                          int64_t first) {
-    typedef ExpertTile<C, OUT, COLS, GATHER> E;
+    typedef ExpertTile<C, OUT, COLS, GATHER, ONCE> E;
     extern __shared__ u32x4 shared[];
     Place at;
     if (!block_tile(a.seg, first, C::BQ, (a.n + E::BP - 1) / E::BP, &at)) return;
@@ -281,8 +281,8 @@ struct GradWeightTiles {
         int expert, q0, p0;
         int start;
     };
-    typedef ColsOperand<C::BQ, C::kThreads, false, false> Q;
-    typedef ColsOperand<C::BP, C::kThreads, GATHER, true> P;
+    typedef ColsOperand<C::BQ, C::kThreads, false, false, false> Q;
+    typedef ColsOperand<C::BP, C::kThreads, GATHER, true, false> P;
     const GradWeightArgs &a;
     const int down, across, wq, wp;
     int64_t id, all, share;
@@ -431,7 +431,7 @@ template <typename C, typename K>
 hipError_t launch_stream(K kernel, const GradWeightArgs &a, int64_t tiles, hipStream_t stream) {
     const hipError_t e = allow_lds(kernel, C::kLds);
     if (e != hipSuccess) return e;
-    const int64_t blocks = (persistent_grid(tiles, 1) + 7) / 8 * 8;
+    const int64_t blocks = (persistent_grid(tiles, C::kLds > 80 * 1024 ? 1 : 2) + 7) / 8 * 8;
     kernel<<<static_cast<uint32_t>(blocks), C::kThreads, C::kLds, stream>>>(a);
     return hipGetLastError();
 }
@@ -444,32 +444,75 @@ int64_t row_tiles(const Segments &s, int per) {
     return (slots < s.num_experts ? slots : s.num_experts) + slots / per;
 }
 
-template <typename C, int OUT, bool COLS>
-hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream) {
+// sums: of how many waves' columns a row's sums are, for kGateGrad.
+template <typename C, int OUT, bool COLS, bool ONCE>
+hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream, int *sums) {
     constexpr int BP = OUT == kGated ? C::BP / 2 : C::BP;
-    const int64_t tiles = row_tiles(a.seg, C::BQ) * ((a.n + BP - 1) / BP);
+    const int across = (a.n + BP - 1) / BP;
+    const int64_t tiles = row_tiles(a.seg, C::BQ) * across;
+    if (sums) *sums = across * C::WP;
     if constexpr (!COLS) {
         if (a.token_rows)
-            return launch_tiles<C>(expert_kernel<C, OUT, COLS, true>, a, tiles, stream);
+            return launch_tiles<C>(expert_kernel<C, OUT, COLS, true, ONCE>, a, tiles, stream);
     }
-    return launch_tiles<C>(expert_kernel<C, OUT, COLS, false>, a, tiles, stream);
+    return launch_tiles<C>(expert_kernel<C, OUT, COLS, false, ONCE>, a, tiles, stream);
 }
 
+// Tile by the rows an expert has on average and the size of the grid, in tiles that there will be
+// at least (64 experts of 7168 channels and 2 x 2048 gated outputs, us; 3.76 GB of weights).
+//   ONCE: an expert has one row tile, and its weights are read past the caches: 16 rows 608 without
+//   and 544 with, 128 tokens of 8 experts 931 and 842 for the whole block.  With several row tiles
+//   the others read them from the caches: 192 rows 793 and 775, but the product down 453 and
+//   469, and the gradient of x 835 and 841.  Few weights may be in the 256 MB last-level cache from
+//   the call before (22 MB: 14.3 without, 18.2 with).
+//   32 rows by 128 outputs up to 16 rows an expert (16 by 128: 544 without ONCE at 2 rows and at 4,
+//   652 at 16, where 32 by 128 takes 609), 64 by 128 up to 48 (24: 638 with 32 by 128, 613; 48: 777
+//   and 629; 64: 746, 256 by 256 630), behind that 256 by 256 (128: 1052 with 64 by 128, 885 with 128
+//   by 128, 780 with 128 by 256, 677).  Weights in columns are read in pieces of 512 bytes by tiles of
+//   256 outputs, of 256 by tiles of 128: the gradient of the activation 16 rows 343 with 32 by 128,
+//   316 with 256 by 256.
+//   A grid that does not fill the card takes smaller tiles (16 experts, 25 rows, 648 channels, 2 x 360
+//   outputs and back: 15.6 with 32 by 128, 14.3 with 16 by 128; one token of 8 experts 124 and 122).
 template <typename T, int OUT, bool COLS>
-hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream) {
+hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream, int *sums = nullptr) {
     const int64_t slots = slots_of(a.seg), experts = a.seg.num_experts;
-    if (slots > 64 * experts) return launch_expert<Tile<T, 256, 256, 2, 4, 2, 3>, OUT, COLS>(a, stream);
-    if (slots > 16 * experts) return launch_expert<Tile<T, 64, 128, 2, 2, 3, 3>, OUT, COLS>(a, stream);
-    if constexpr (COLS)
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
-    else
-        return launch_expert<Tile<T, 16, 128, 1, 4, 4, 4>, OUT, COLS>(a, stream);
+    const int64_t active = slots < experts ? slots : experts;
+    const int64_t columns = (OUT == kGated ? 2 : 1) * static_cast<int64_t>(a.n);
+    auto tiles = [&](int rows, int cols) {
+        return (slots / rows > active ? slots / rows : active) * ((columns + cols - 1) / cols);
+    };
+    const bool few = slots <= 48 * experts;
+    const bool once = few && active * columns * a.k * T::kBytes > (int64_t(64) << 20);
+    if ((COLS || !few) && tiles(256, 256) >= 256) {
+        typedef Tile<T, 256, 256, 2, 4, 2, 3> C;
+        if constexpr (COLS)
+            if (once) return launch_expert<C, OUT, COLS, true>(a, stream, sums);
+        return launch_expert<C, OUT, COLS, false>(a, stream, sums);
+    }
+    if (slots > 16 * experts && tiles(64, 128) >= 512) {
+        typedef Tile<T, 64, 128, 2, 2, 3, 3> C;
+        return once ? launch_expert<C, OUT, COLS, true>(a, stream, sums)
+                    : launch_expert<C, OUT, COLS, false>(a, stream, sums);
+    }
+    if (tiles(32, 128) >= 512) {
+        typedef Tile<T, 32, 128, 1, 4, 4, 4> C;
+        return once ? launch_expert<C, OUT, COLS, true>(a, stream, sums)
+                    : launch_expert<C, OUT, COLS, false>(a, stream, sums);
+    }
+    typedef Tile<T, 16, 128, 1, 4, 4, 4> C;
+    return once ? launch_expert<C, OUT, COLS, true>(a, stream, sums)
+                : launch_expert<C, OUT, COLS, false>(a, stream, sums);
+}
+
+int64_t grad_tiles(const GradWeightArgs &a, int size) {
+    return static_cast<int64_t>(a.seg.num_experts) * ((a.n + size - 1) / size) *
+           ((a.k + size - 1) / size);
 }
 
 }  // namespace
 
-// A wave's sums are of 64 columns.
-int gate_grad_tiles(int32_t inter) { return (inter + 255) / 256 * 4; }
+// A wave's sums are of 32 columns at least.
+int gate_grad_tiles(int32_t inter) { return (inter + 127) / 128 * 4; }
 
 hipError_t launch_expert_i8(const ExpertArgs &a, bool gated, hipStream_t stream) {
     return gated ? choose_expert<Int8, kGated, false>(a, stream)
@@ -486,11 +529,12 @@ hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t stream) {
 
 hipError_t launch_expert_gate_grad(const ExpertArgs &a, float *grad_row_weights, const int32_t *dst,
                                    hipStream_t stream) {
-    hipError_t e = launch_expert<Tile<Bf16, 256, 256, 2, 4, 2, 3>, kGateGrad, true>(a, stream);
+    int tiles = 0;
+    const hipError_t e = choose_expert<Bf16, kGateGrad, true>(a, stream, &tiles);
     if (e != hipSuccess || !grad_row_weights) return e;
     const int64_t slots = slots_of(a.seg), blocks = (slots + 255) / 256;
     row_sums_kernel<<<static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
-        dst, a.seg.scalars, slots, a.seg.capacity, a.partial, gate_grad_tiles(a.n),
+        dst, a.seg.scalars, slots, a.seg.capacity, a.partial, tiles,
         grad_row_weights);
     return hipGetLastError();
 }
@@ -499,15 +543,23 @@ hipError_t launch_expert_grad_rows(const ExpertArgs &a, hipStream_t stream) {
     return choose_expert<Bf16, kPlain, true>(a, stream);
 }
 
-hipError_t launch_expert_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
-    typedef Tile<Bf16, 256, 256, 2, 4, 2, 3> C;
-    const int64_t tiles = static_cast<int64_t>(a.seg.num_experts) * ((a.n + C::BQ - 1) / C::BQ) *
-                          ((a.k + C::BP - 1) / C::BP);
+template <typename C>
+static hipError_t launch_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
+    const int64_t tiles = grad_tiles(a, C::BQ);
     if (a.f32)
         return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, true>, a, tiles, stream)
                             : launch_stream<C>(grad_weight_kernel<C, false, true>, a, tiles, stream);
     return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, false>, a, tiles, stream)
                         : launch_stream<C>(grad_weight_kernel<C, false, false>, a, tiles, stream);
+}
+
+// Tiles of 256 x 256 where they fill the card, else of 128 x 128 (16 experts of 128 rows, us: 144 large
+// tiles 12.0 and 11.4, 128 15.2 and 11.5, 96 8.9 and 7.2; 256 13.7 and 13.9; 32 experts, 2048
+// 105 and 116).
+hipError_t launch_expert_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
+    return grad_tiles(a, 256) >= 192
+               ? launch_grad_weight<Tile<Bf16, 256, 256, 2, 4, 2, 3>>(a, stream)
+               : launch_grad_weight<Tile<Bf16, 128, 128, 2, 2, 2, 3>>(a, stream);
 }
 
 }  // namespace ep

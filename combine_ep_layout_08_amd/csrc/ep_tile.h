@@ -72,9 +72,15 @@ __device__ inline const char *uniform(const void *p) {
 // 16 bytes a lane from memory to LDS at `to` + 16 lane, `to` the same in all lanes.  The
 // compiler does not count these loads: wait_loads() does.  (Its builtin makes it wait for all
 // of them before any read of LDS.)  Lanes that are switched off write nothing.
+// ONCE: past the caches.
+template <bool ONCE>
 __device__ inline void load_lds(uint32_t to, const char *base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(to), "v"(off), "s"(base) : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                     :: "s"(to), "v"(off), "s"(base) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :: "s"(to), "v"(off), "s"(base) : "memory");
 }
 
 __device__ inline void load_lds(uint32_t to, const char *from) {
@@ -115,7 +121,7 @@ __device__ inline int64_t token_of(const int32_t *src_meta, int64_t row, int top
 // An operand of R rows in rows of channels.  `Threads` threads bring a chunk in kLoads loads
 // each: load i takes row i * Threads / 8 + thread / 8.  `row_of(i)` gives the row's byte offset
 // from `base` (GATHER: its address).
-template <int R, int Threads, bool GATHER>
+template <int R, int Threads, bool GATHER, bool ONCE>
 struct RowsOperand {
     static constexpr int kBytes = R * 128;
     static constexpr int kLoads = kBytes / (Threads * 16) > 0 ? kBytes / (Threads * 16) : 1;
@@ -152,7 +158,7 @@ struct RowsOperand {
             load_lds(stage + to + i * Threads * 16, from[i]);
             from[i] += 128;
         } else {
-            load_lds(stage + to + i * Threads * 16, base, off[i]);
+            load_lds<ONCE>(stage + to + i * Threads * 16, base, off[i]);
         }
     }
     __device__ void advance() {
@@ -178,7 +184,7 @@ struct RowsOperand {
 // matrix instructions are dealt out so that a lane's sums lie side by side, part l / 16 of the
 // wave's columns having 4 in each instruction: the transposing read takes any four columns
 // that lie together.
-template <int C, int Threads, bool GATHER, bool CONSECUTIVE>
+template <int C, int Threads, bool GATHER, bool CONSECUTIVE, bool ONCE>
 struct ColsOperand {
     static constexpr int kRow = 2 * C;                       // bytes of a channel
     static constexpr int kBytes = 64 * kRow;
@@ -223,7 +229,7 @@ struct ColsOperand {
     // Load i of the next chunk to `stage`, all of its channels; advance() after the last one.
     __device__ void load(uint32_t stage, int i) {
         if (GATHER) load_lds(stage + to + i * Threads * 16, address(i));
-        else load_lds(stage + to + i * Threads * 16, uniform(base), off[i]);
+        else load_lds<ONCE>(stage + to + i * Threads * 16, uniform(base), off[i]);
     }
     __device__ void advance() {
         if (GATHER) src_meta += 64;

@@ -183,6 +183,17 @@ I8_CASES = [  # T, K, E, A, k, n, gated, weights, token rows, empty
     (96, 8, 300, 8, 256, 64, False, False, False, 0.1),
     (3, 2, 1000, 1, 128, 16, True, True, True, 0.0),
     (5, 2, 4, 1, 32768, 32, False, False, False, 0.0),
+    # tiles of 32 rows, of 64, of 256 (more outputs fill the card), and weights of more than 64 MB
+    # read past the caches in tiles of 16, 32 and 64 rows
+    (40, 4, 16, 1, 80, 4112, False, False, True, 0.1),
+    (40, 4, 16, 1, 80, 4112, True, True, False, 0.1),
+    (130, 4, 16, 8, 144, 4104, False, False, False, 0.1),
+    (130, 4, 16, 1, 144, 4112, True, False, True, 0.0),
+    (700, 2, 3, 8, 208, 9528, False, False, True, 0.0),
+    (700, 2, 3, 1, 336, 9552, True, True, False, 0.1),
+    (3, 2, 4, 1, 5136, 4096, False, False, True, 0.0),
+    (20, 4, 8, 1, 2064, 8208, True, True, True, 0.1),
+    (60, 4, 8, 1, 1040, 8200, False, False, False, 0.1),
 ]
 
 
@@ -389,6 +400,16 @@ FFN_CASES = [  # T, K, E, A, H, I, token rows, weights, empty
     (520, 2, 3, 8, 384, 144, False, True, 0.1),
     (600, 3, 4, 1, 136, 264, True, False, 0.0),
     (40, 4, 300, 2, 64, 24, False, True, 0.1),
+    # tiles of 32, 64 and 256 rows, for one of the products each; large tiles of the weights' gradients;
+    # weights of more than 64 MB, read past the caches
+    (40, 4, 16, 1, 72, 2056, True, True, 0.1),
+    (130, 4, 16, 8, 4104, 40, False, True, 0.1),
+    (130, 4, 16, 1, 88, 2064, False, False, 0.0),
+    (700, 2, 3, 8, 72, 8200, False, True, 0.1),
+    (700, 2, 3, 1, 9528, 40, True, False, 0.0),
+    (3, 2, 4, 1, 2056, 4104, True, True, 0.0),
+    (30, 4, 8, 1, 1032, 4104, False, True, 0.1),
+    (60, 4, 8, 1, 8200, 520, True, False, 0.1),
 ]
 
 

@@ -1,5 +1,6 @@
 // The experts' products on gfx950 (include/ep_expert.h): int8 rows and weights, the bf16
 // gated feed-forward block, and its gradients.
+#include <atomic>
 #include <type_traits>
 
 #include "ep_expert_internal.h"
@@ -402,24 +403,32 @@ __global__ __launch_bounds__(256) void row_sums_kernel(const int32_t *dst, const
 }
 
 // ---------------------------------------------------------------- launches
-// Kernels with more than 64 KB of LDS have to say so once a device.
-template <typename K>
-hipError_t allow_lds(K kernel, int bytes) {
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Kernels with more than 64 KB of LDS have to say so, once a device.
+template <auto Kernel>
+hipError_t allow_lds(int bytes) {
+    static std::atomic<uint64_t> said{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (said.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess && dev < 64) said.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 constexpr int64_t kMostBlocks = int64_t(1) << 22;    // of a launch; a multiple of 8
 
 // A block for every tile.
-template <typename C, typename K>
-hipError_t launch_tiles(K kernel, const ExpertArgs &a, int64_t tiles, hipStream_t stream) {
-    hipError_t e = allow_lds(kernel, C::kLds);
+template <typename C, auto Kernel>
+hipError_t launch_tiles(const ExpertArgs &a, int64_t tiles, hipStream_t stream) {
+    hipError_t e = allow_lds<Kernel>(C::kLds);
     if (e != hipSuccess) return e;
     const int64_t blocks = (tiles + 7) / 8 * 8;
     for (int64_t b = 0; b < blocks; b += kMostBlocks) {
         const int64_t n = blocks - b < kMostBlocks ? blocks - b : kMostBlocks;
-        kernel<<<static_cast<uint32_t>(n), C::kThreads, C::kLds, stream>>>(a, b);
+        Kernel<<<static_cast<uint32_t>(n), C::kThreads, C::kLds, stream>>>(a, b);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -427,12 +436,12 @@ hipError_t launch_tiles(K kernel, const ExpertArgs &a, int64_t tiles, hipStream_
 }
 
 // A block for every compute unit, which walks the tiles.
-template <typename C, typename K>
-hipError_t launch_stream(K kernel, const GradWeightArgs &a, int64_t tiles, hipStream_t stream) {
-    const hipError_t e = allow_lds(kernel, C::kLds);
+template <typename C, auto Kernel>
+hipError_t launch_stream(const GradWeightArgs &a, int64_t tiles, hipStream_t stream) {
+    const hipError_t e = allow_lds<Kernel>(C::kLds);
     if (e != hipSuccess) return e;
     const int64_t blocks = (persistent_grid(tiles, C::kLds > 80 * 1024 ? 1 : 2) + 7) / 8 * 8;
-    kernel<<<static_cast<uint32_t>(blocks), C::kThreads, C::kLds, stream>>>(a);
+    Kernel<<<static_cast<uint32_t>(blocks), C::kThreads, C::kLds, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -453,9 +462,9 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream, int *sums) {
     if (sums) *sums = across * C::WP;
     if constexpr (!COLS) {
         if (a.token_rows)
-            return launch_tiles<C>(expert_kernel<C, OUT, COLS, true, ONCE>, a, tiles, stream);
+            return launch_tiles<C, expert_kernel<C, OUT, COLS, true, ONCE>>(a, tiles, stream);
     }
-    return launch_tiles<C>(expert_kernel<C, OUT, COLS, false, ONCE>, a, tiles, stream);
+    return launch_tiles<C, expert_kernel<C, OUT, COLS, false, ONCE>>(a, tiles, stream);
 }
 
 // Tile by the rows an expert has on average and the size of the grid, in tiles that there will be
@@ -547,10 +556,10 @@ template <typename C>
 static hipError_t launch_grad_weight(const GradWeightArgs &a, hipStream_t stream) {
     const int64_t tiles = grad_tiles(a, C::BQ);
     if (a.f32)
-        return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, true>, a, tiles, stream)
-                            : launch_stream<C>(grad_weight_kernel<C, false, true>, a, tiles, stream);
-    return a.token_rows ? launch_stream<C>(grad_weight_kernel<C, true, false>, a, tiles, stream)
-                        : launch_stream<C>(grad_weight_kernel<C, false, false>, a, tiles, stream);
+        return a.token_rows ? launch_stream<C, grad_weight_kernel<C, true, true>>(a, tiles, stream)
+                            : launch_stream<C, grad_weight_kernel<C, false, true>>(a, tiles, stream);
+    return a.token_rows ? launch_stream<C, grad_weight_kernel<C, true, false>>(a, tiles, stream)
+                        : launch_stream<C, grad_weight_kernel<C, false, false>>(a, tiles, stream);
 }
 
 // Tiles of 256 x 256 where they fill the card, else of 128 x 128 (16 experts of 128 rows, us: 144 large

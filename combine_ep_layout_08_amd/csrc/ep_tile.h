@@ -77,15 +77,15 @@ template <bool ONCE>
 __device__ inline void load_lds(uint32_t to, const char *base, uint32_t off) {
     if constexpr (ONCE)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
-                     :: "s"(to), "v"(off), "s"(base) : "memory");
+                     :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                     :: "s"(to), "v"(off), "s"(base) : "memory");
+                     :: "s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
 
 __device__ inline void load_lds(uint32_t to, const char *from) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(to), "v"(from) : "memory");
+                 :: "s"(to), "v"(from) : "memory", "m0");
 }
 
 // Until at most N of the wave's loads are under way, and its LDS stores are done.

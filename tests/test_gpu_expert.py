@@ -589,3 +589,113 @@ def test_after_a_capacity_error_nothing_is_written():
                 torch.ones((E, 16, H), dtype=torch.int8, device="cuda"),
                 torch.ones((E, 16), device="cuda"), out=o)
     assert ref.untouched(o, b.rows)
+
+
+# ---------------------------------------------------------------- far apart, and long
+
+def test_offsets_past_32_bits_in_rows():
+    """Segments 4.3 GB and more behind the buffers' start: rows of 32 KB, segments of 65536 rows."""
+    T, E, A, H, I = 9, 3, 65536, 16384, 40
+    idx = (torch.arange(T, device="cuda") % E)[:, None].contiguous()
+    h = ep.Handle(T, 1, E, A)
+    h.layout(idx)
+    rows, expert, token = ref.rows_of(h, idx)
+    assert int(rows.max()) * H * 2 > 2 ** 32 and h.capacity * H > 2 ** 31
+    gen = _gen(21)
+    b = Block.__new__(Block)
+    b.h, b.idx, b.rows, b.expert, b.token = h, idx, rows, expert, token
+    b.E, b.H, b.I, b.token_rows, b.rw = E, H, I, False, None
+    b.w13, b.w2 = _randn((E, 2 * I, H), gen, H ** -0.5), _randn((E, H, I), gen, I ** -0.5)
+    b.x = torch.zeros((h.capacity, H), dtype=torch.bfloat16, device="cuda")
+    b.grad = torch.zeros_like(b.x)
+    b.x[rows], b.grad[rows] = _randn((T, H), gen), _randn((T, H), gen, 0.1)
+    y, hh, saved = h.expert_ffn(b.x, b.w13, b.w2, want_saved=True)
+    gx, g13, g2, _, ggu = h.expert_ffn_backward(b.grad, b.x, b.w13, b.w2, saved, hh)
+    far = int(rows.max())
+    at = (rows == far).nonzero().item()
+    e = int(expert[at])
+    x64, w = b.x[far].double(), b.w13[e].double()
+    v = w @ x64
+    tol = (w.abs() @ x64.abs()) * _sum_tol(H) + v.abs() * BF16
+    ref.assert_close(saved[far], v, tol, "far gate_up")
+    want = b.w2[e].double() @ hh[far].double()
+    tol = (b.w2[e].double().abs() @ hh[far].double().abs()) * _sum_tol(I) + want.abs() * BF16
+    ref.assert_close(y[far], want, tol, "far y")
+    want = ggu[far].double() @ w
+    tol = (ggu[far].double().abs() @ w.abs()) * _sum_tol(2 * I) + want.abs() * BF16 + 1e-38
+    ref.assert_close(gx[far], want, tol, "far grad x")
+    mine = rows[expert == e]
+    for got, p, q in ((g13[e], ggu[mine].double(), b.x[mine].double()),
+                      (g2[e], b.grad[mine].double(), hh[mine].double())):
+        want = p.t() @ q
+        ref.assert_close(got, want, (p.abs().t() @ q.abs()) * _sum_tol(mine.numel()) +
+                         want.abs() * BF16 + 1e-38, "far weight gradient")
+    n = 16400
+    q, s = h.quantize_i8(b.x)
+    wq = torch.randint(-127, 128, (E, n, H), generator=gen, device="cuda", dtype=torch.int8)
+    ws = torch.rand((E, n), generator=gen, device="cuda") * 0.01
+    out = h.expert_i8(q, s, wq, ws)
+    assert torch.equal(q[far], _codes64(b.x[far][None])[0][0])
+    want = (wq[e].double() @ q[far].double()) * s[far].double() * ws[e].double()
+    ref.assert_close(out[far], want, want.abs() * (BF16 + 4 * F32) + 1e-38, "far int8")
+
+
+def test_offsets_past_32_bits_in_weights():
+    """The widest block: 32768 channels of h, weights of 4.8 GB in both projections."""
+    T, E, H, I = 5, 3, 12288, 32768
+    gen = _gen(22)
+    idx = torch.tensor([[2], [0], [2], [1], [2]], device="cuda")
+    h = ep.Handle(T, 1, E, 1)
+    h.layout(idx)
+    rows, expert, token = ref.rows_of(h, idx)
+    w13 = (torch.randn((E, 2 * I, H), generator=gen, device="cuda", dtype=torch.float32)
+           .mul_(H ** -0.5).bfloat16())
+    w2 = _randn((E, H, I), gen, I ** -0.5)
+    assert w13.numel() * 2 > 2 ** 32
+    x, grad = _randn((T, H), gen), _randn((h.capacity, H), gen, 0.1)
+    y, hh, saved = h.expert_ffn(x, w13, w2, token_rows=True, want_saved=True)
+    gx, g13, g2, _, ggu = h.expert_ffn_backward(grad, x, w13, w2, saved, hh, token_rows=True)
+    e, mine = 2, expert == 2
+    r, src = rows[mine], token[mine]
+    for name, got, p, w in (("gate_up", saved, x[src], w13[e]), ("y", y, hh[r], w2[e])):
+        for part in range(0, w.shape[0], 8192):
+            wp = w[part:part + 8192].double()
+            want = p.double() @ wp.t()
+            tol = (p.double().abs() @ wp.abs().t()) * _sum_tol(w.shape[1]) + want.abs() * BF16 + 1e-38
+            ref.assert_close(got[r, part:part + 8192], want, tol, f"{name} {part}")
+    want, tol = torch.zeros((len(r), H), dtype=torch.float64, device="cuda"), 0
+    for part in range(0, 2 * I, 8192):
+        gp, wp = ggu[r, part:part + 8192].double(), w13[e, part:part + 8192].double()
+        want += gp @ wp
+        tol = tol + (gp.abs() @ wp.abs()) * _sum_tol(2 * I)
+        full = gp.t() @ x[src].double()
+        ref.assert_close(g13[e, part:part + 8192], full, full.abs() * BF16 +
+                         (gp.abs().t() @ x[src].double().abs()) * _sum_tol(3) + 1e-38, f"w13 {part}")
+    ref.assert_close(gx[r], want, tol + want.abs() * BF16 + 1e-38, "grad x")
+    full = grad[r].double().t() @ hh[r].double()
+    ref.assert_close(g2[e], full, full.abs() * BF16 + (grad[r].double().abs().t() @
+                     hh[r].double().abs()) * _sum_tol(3) + 1e-38, "w2")
+
+
+def test_many_tiles_a_block_and_few_rows_between_many():
+    """Weight gradients of more tiles than blocks, experts of none, one and many rows in turns: a
+    block goes from tiles of one chunk to tiles of many and back."""
+    gen = _gen(23)
+    E, H, I = 24, 520, 1032
+    counts = [0, 1, 700, 2, 0, 64, 65, 1, 1, 63, 300, 0, 128, 3, 0, 0, 5, 200, 1, 64, 1, 1, 129, 0]
+    ids = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    idx = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(1))][:, None].cuda()
+    for token_rows in (False, True):
+        b = Block(len(ids), 1, E, 4, H, I, token_rows, True, 0.0, 24)
+        b.h.layout(idx)
+        b.idx = idx
+        b.rows, b.expert, b.token = ref.rows_of(b.h, idx)
+        b.grad = _spoil(_randn(b.grad.shape, gen, 0.1), b.rows)
+        b.rw = _spoil(torch.rand(b.rw.shape, generator=gen, device="cuda"), b.rows)
+        b.x = _randn(b.x.shape, gen)
+        if not token_rows:
+            _spoil(b.x, b.rows)
+        y, h, saved = b.forward()
+        b.check_forward(y, h, saved)
+        for dtype in (torch.bfloat16, torch.float32):
+            b.check_backward(saved, h, b.backward(saved, h, dtype), False)

@@ -38,7 +38,7 @@ __all__ = [
     "add_rmsnorm_backward", "pack_w4",
     "ep_quantize_i8", "ep_quantize_i8_rows", "ep_expert_i8", "ep_expert_ffn",
     "ep_expert_ffn_backward", "ep_expert_ffn_backward_workspace", "quantize_i8",
-    "bind_quantize_i8",
+    "bind_quantize_i8", "bind_expert_i8", "bind_expert_ffn",
 ]
 
 LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(
@@ -574,10 +574,35 @@ def quantize_i8(x: torch.Tensor, out_q=None, out_scale=None):
     return result
 
 
-def bind_quantize_i8(x: torch.Tensor, out_q=None, out_scale=None) -> "BoundCall":
-    """``quantize_i8`` bound to these tensors (see BoundCall)."""
-    fn, args, result, keep = _quantize_i8_call(x, out_q, out_scale)
-    return BoundCall(fn, args, "ep_quantize_i8", result, keep)
+def bind_quantize_i8(x: torch.Tensor, out_q=None, out_scale=None,
+                     handle: Optional["Handle"] = None) -> "BoundCall":
+    """``quantize_i8``, or with a ``handle`` ``Handle.quantize_i8`` of its expert rows, bound to
+    these tensors (see BoundCall)."""
+    if handle is None:
+        fn, args, result, keep = _quantize_i8_call(x, out_q, out_scale)
+        return BoundCall(fn, args, "ep_quantize_i8", result, keep)
+    fn, args, result, keep = handle._quantize_i8_call(x, out_q, out_scale)
+    return BoundCall(fn, args, "ep_quantize_i8_rows", result, (handle, keep), handle.h)
+
+
+def bind_expert_i8(handle: "Handle", x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor,
+                   w_scale: torch.Tensor, gated: bool = False,
+                   row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
+                   out: Optional[torch.Tensor] = None) -> "BoundCall":
+    """``handle.expert_i8`` bound to these tensors (see BoundCall)."""
+    fn, args, out, keep = handle._expert_i8_call(x, x_scale, w, w_scale, gated, row_weights,
+                                                 token_rows, out)
+    return BoundCall(fn, args, "ep_expert_i8", out, (handle, keep), handle.h)
+
+
+def bind_expert_ffn(handle: "Handle", x: torch.Tensor, w13: torch.Tensor,
+                    w2: Optional[torch.Tensor], row_weights: Optional[torch.Tensor] = None,
+                    token_rows: bool = False, want_saved: bool = False, out_h=None, saved=None,
+                    out=None) -> "BoundCall":
+    """``handle.expert_ffn`` bound to these tensors (see BoundCall)."""
+    fn, args, result, keep = handle._expert_ffn_call(x, w13, w2, row_weights, token_rows,
+                                                     want_saved, out_h, saved, out)
+    return BoundCall(fn, args, "ep_expert_ffn", result, (handle, keep), handle.h)
 
 
 _CODE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
@@ -1449,11 +1474,6 @@ class Handle:
         _check(fn(*args, _stream()), "ep_quantize_i8_rows")
         return result
 
-    def bind_quantize_i8(self, x: torch.Tensor, out_q=None, out_scale=None) -> BoundCall:
-        """``quantize_i8`` bound to these tensors (see BoundCall)."""
-        fn, args, result, keep = self._quantize_i8_call(x, out_q, out_scale)
-        return BoundCall(fn, args, "ep_quantize_i8_rows", result, (self, keep), self.h)
-
     def _quantize_i8_call(self, x, out_q, out_scale):
         out_q, out_scale = _i8_rows(x, self.capacity, "capacity", out_q, out_scale)
         _here(x, out_q, out_scale, self.workspace)
@@ -1474,15 +1494,6 @@ class Handle:
                                                 token_rows, out)
         _check(fn(*args, _stream()), "ep_expert_i8")
         return out
-
-    def bind_expert_i8(self, x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor,
-                       w_scale: torch.Tensor, gated: bool = False,
-                       row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
-                       out: Optional[torch.Tensor] = None) -> BoundCall:
-        """``expert_i8`` bound to these tensors (see BoundCall)."""
-        fn, args, out, keep = self._expert_i8_call(x, x_scale, w, w_scale, gated, row_weights,
-                                                   token_rows, out)
-        return BoundCall(fn, args, "ep_expert_i8", out, (self, keep), self.h)
 
     def _expert_i8_call(self, x, x_scale, w, w_scale, gated, row_weights, token_rows, out):
         E, rows = self.h.num_experts, self.h.num_tokens if token_rows else self.capacity
@@ -1518,14 +1529,6 @@ class Handle:
                                                     want_saved, out_h, saved, out)
         _check(fn(*args, _stream()), "ep_expert_ffn")
         return result
-
-    def bind_expert_ffn(self, x: torch.Tensor, w13: torch.Tensor, w2: Optional[torch.Tensor],
-                        row_weights: Optional[torch.Tensor] = None, token_rows: bool = False,
-                        want_saved: bool = False, out_h=None, saved=None, out=None) -> BoundCall:
-        """``expert_ffn`` bound to these tensors (see BoundCall)."""
-        fn, args, result, keep = self._expert_ffn_call(x, w13, w2, row_weights, token_rows,
-                                                       want_saved, out_h, saved, out)
-        return BoundCall(fn, args, "ep_expert_ffn", result, (self, keep), self.h)
 
     def _ffn_sizes(self, w13, w2):
         E = self.h.num_experts

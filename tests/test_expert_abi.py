@@ -1,8 +1,10 @@
 """The C entries of the experts' products and their binding on the CPU: exported functions,
 sizes, and every refusal, none of which reaches a HIP runtime function; and the binding's
 arguments, with a fake library in place of the real one."""
+import gc
 import os
 import re
+import weakref
 
 import pytest
 import torch
@@ -215,7 +217,7 @@ def test_binding_quantiser(fake):
     q, s = h.quantize_i8(y)
     assert fake.last("ep_quantize_i8_rows")[1:] == (y.data_ptr(), 32, q.data_ptr(), s.data_ptr(),
                                                     STREAM)
-    assert h.bind_quantize_i8(y, q, s)() == (q, s)
+    assert ep.bind_quantize_i8(y, q, s, handle=h)() == (q, s)
     for bad in (lambda: ep.quantize_i8(x.float()), lambda: ep.quantize_i8(x[0]),
                 lambda: ep.quantize_i8(x, out_q=_i8(6, 32)), lambda: ep.quantize_i8(x.t()),
                 lambda: ep.quantize_i8(x, out_scale=torch.zeros(5)), lambda: h.quantize_i8(x)):
@@ -234,7 +236,7 @@ def test_binding_i8(fake):
         out.data_ptr(), STREAM)
     cap = h.capacity
     x, xs = _i8(cap, 64), torch.ones(cap)
-    call = h.bind_expert_i8(x, xs, w, ws)
+    call = ep.bind_expert_i8(h, x, xs, w, ws)
     assert call().shape == (cap, 32)
     a = fake.last("ep_expert_i8")
     assert a[3] == 0 and a[8:10] == (0, None)
@@ -261,7 +263,7 @@ def test_binding_ffn(fake):
     assert fake.last("ep_expert_ffn")[1:] == (
         x.data_ptr(), 0, 64, w13.data_ptr(), w2.data_ptr(), 24, rw.data_ptr(), hh.data_ptr(),
         saved.data_ptr(), y.data_ptr(), STREAM)
-    y, hh, none = h.bind_expert_ffn(_bf16(16, 64), w13, None, token_rows=True)()
+    y, hh, none = ep.bind_expert_ffn(h, _bf16(16, 64), w13, None, token_rows=True)()
     a = fake.last("ep_expert_ffn")
     assert y is None and none is None and a[2] == 1 and a[5] is None and a[9:11] == (None, None)
     for bad in (lambda: h.expert_ffn(x, w13, w2, token_rows=True),
@@ -308,3 +310,28 @@ def test_binding_ffn_gradients(fake):
                                               workspace=torch.zeros(64))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_bound_calls_keep_the_handles_workspace(fake):
+    """The kernels read counts, rows and the error word in the handle's workspace: a bound call
+    that outlives the caller's handle holds it, and refuses another batch's size."""
+    def calls(h):
+        cap = h.capacity
+        yield ep.bind_quantize_i8(_bf16(cap, 32), handle=h)
+        yield ep.bind_expert_i8(h, _i8(cap, 64), torch.ones(cap), _i8(8, 32, 64), torch.ones(8, 32))
+        yield ep.bind_expert_ffn(h, _bf16(cap, 64), _bf16(8, 48, 64), _bf16(8, 64, 24))
+
+    for i in range(3):
+        h = _handle()
+        workspace = weakref.ref(h.workspace)
+        call = list(calls(h))[i]
+        del h
+        gc.collect()
+        assert workspace() is not None
+        call()
+        call._h.num_tokens = 3
+        with pytest.raises(ValueError, match="bound for 16 tokens"):
+            call()
+        del call
+        gc.collect()
+        assert workspace() is None

@@ -218,10 +218,10 @@ def test_bound_calls_give_what_the_methods_give():
     y = _randn((24, 256), gen)
     quant = ep.bind_quantize_i8(y)
     q, sc = quant()
-    up = h.bind_expert_i8(q, sc, s.w13, s.s13, gated=True, token_rows=True)
-    rows_q = h.bind_quantize_i8(up())
-    down = h.bind_expert_i8(*rows_q(), s.w2, s.s2)
-    block = h.bind_expert_ffn(y, _randn((8, 128, 256), gen, 0.1), _randn((8, 256, 64), gen, 0.1),
+    up = ep.bind_expert_i8(h, q, sc, s.w13, s.s13, gated=True, token_rows=True)
+    rows_q = ep.bind_quantize_i8(up(), handle=h)
+    down = ep.bind_expert_i8(h, *rows_q(), s.w2, s.s2)
+    block = ep.bind_expert_ffn(h, y, _randn((8, 128, 256), gen, 0.1), _randn((8, 256, 64), gen, 0.1),
                               token_rows=True)
     for _ in range(2):
         y.copy_(_randn(y.shape, gen))

@@ -202,8 +202,8 @@ def prepare(case, seed):
         s["scale"] = torch.zeros(rows, device=dev)
         if own:
             import combine_ep_layout_08_amd as ep
-            bind = ep.bind_quantize_i8 if tokens else h.bind_quantize_i8
-            s["call"] = bind(s["x"], out_q=s["q"], out_scale=s["scale"])
+            s["call"] = ep.bind_quantize_i8(s["x"], out_q=s["q"], out_scale=s["scale"],
+                                            handle=None if tokens else h)
         return s
     if op == "i8":
         k, n = case["k"], case["n"]
@@ -215,9 +215,10 @@ def prepare(case, seed):
         s["out"] = torch.zeros((cap, n // 2 if case["gated"] else n), dtype=torch.bfloat16,
                                device=dev)
         if own:
-            s["call"] = h.bind_expert_i8(s["x"], s["scale"], s["w"], s["w_scale"],
-                                         gated=case["gated"], row_weights=s["weights"],
-                                         token_rows=tokens, out=s["out"])
+            import combine_ep_layout_08_amd as ep
+            s["call"] = ep.bind_expert_i8(h, s["x"], s["scale"], s["w"], s["w_scale"],
+                                          gated=case["gated"], row_weights=s["weights"],
+                                          token_rows=tokens, out=s["out"])
         return s
     H, I = case["hidden"], case["inter"]  # noqa: E741
     s["x"] = _normal((rows, H), gen, dev)
@@ -229,9 +230,10 @@ def prepare(case, seed):
         s["h"], s["y"] = torch.zeros((cap, I), **like), torch.zeros((cap, H), **like)
         s["saved"] = torch.zeros((cap, 2 * I), **like) if case["save"] else None
         if own:
-            s["call"] = h.bind_expert_ffn(s["x"], s["w13"], s["w2"], row_weights=s["weights"],
-                                          token_rows=tokens, out_h=s["h"], saved=s["saved"],
-                                          out=s["y"])
+            import combine_ep_layout_08_amd as ep
+            s["call"] = ep.bind_expert_ffn(h, s["x"], s["w13"], s["w2"], row_weights=s["weights"],
+                                           token_rows=tokens, out_h=s["h"], saved=s["saved"],
+                                           out=s["y"])
         return s
     s["handle"] = h
     s["grad"] = _normal((cap, H), gen, dev, 1e-2)

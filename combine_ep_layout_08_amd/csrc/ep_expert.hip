@@ -21,6 +21,7 @@ struct Place {
     int expert;              // -1: no such tile
     int start, rows;         // rows of the layout
     int column;              // tile of outputs
+    int tiles;               // row tiles of the expert
 };
 
 // Block `id` of those of a launch: blocks go round the 8 XCDs, each with an L2 of its own, so
@@ -48,7 +49,7 @@ __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int 
     }
     all *= across;
     const int64_t part = (all + 7) / 8, tile = (id & 7) * part + (id >> 3);
-    if ((id >> 3) >= part || tile >= all) return {-1, 0, 0, 0};
+    if ((id >> 3) >= part || tile >= all) return {-1, 0, 0, 0, 0};
     int pass = static_cast<int>(tile / across);
     int64_t before = 0;      // row tiles of the experts so far
     for (int e0 = 0; e0 < experts; e0 += 64) {
@@ -68,9 +69,9 @@ __device__ inline Place find_tile(const Segments &seg, int64_t id, int per, int 
         const int size = ((rows + tiles - 1) / tiles + 15) / 16 * 16;
         const int first = at % tiles * size;
         return {e0 + l, __builtin_amdgcn_readlane(start, l) + first,
-                rows - first < size ? rows - first : size, at / tiles};
+                rows - first < size ? rows - first : size, at / tiles, tiles};
     }
-    return {-1, 0, 0, 0};
+    return {-1, 0, 0, 0, 0};
 }
 
 // The tile of a block of a launch, inside the rows' buffers whatever the layout holds.
@@ -84,6 +85,7 @@ __device__ inline bool block_tile(const Segments &seg, int64_t first, int per, i
     p->start = __builtin_amdgcn_readfirstlane(p->start);
     p->rows = __builtin_amdgcn_readfirstlane(p->rows);
     p->column = __builtin_amdgcn_readfirstlane(p->column);
+    p->tiles = __builtin_amdgcn_readfirstlane(p->tiles);
     if (p->start < 0 || p->start >= seg.capacity) return false;
     if (p->rows > seg.capacity - p->start) p->rows = static_cast<int>(seg.capacity - p->start);
     return true;
@@ -254,6 +256,18 @@ struct ExpertTile {
     }
 };
 
+// The tile's sums, operands as E has them.
+template <typename E, typename C>
+__device__ inline void expert_sums(const ExpertArgs &a, const Place &at, uint32_t lds,
+                                   typename C::Sums &sums) {
+    const E tile{a, at};
+    typename E::Q q;
+    typename E::P p;
+    tile.start_q(q);
+    tile.start_p(p);
+    expert_product<C>(q, p, a.k, at.rows, lds, sums);
+}
+
 template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const ExpertArgs a,
                                                                          int64_t first) {
@@ -261,14 +275,16 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
     extern __shared__ u32x4 shared[];
     Place at;
     if (!block_tile(a.seg, first, C::BQ, (a.n + E::BP - 1) / E::BP, &at)) return;
-    const E tile{a, at};
-    typename E::Q q;
-    typename E::P p;
     typename C::Sums sums;
-    tile.start_q(q);
-    tile.start_p(p);
-    expert_product<C>(q, p, a.k, at.rows, lds_address(shared), sums);
-    tile.finish(sums);
+    // row tiles that follow each other find an expert's weights in the L2 if the first left them there
+    // (64 experts, 4 x 7168 x 2048, us: 2048 rows all on one 276 past the caches, 230 not; half of
+    // 3040 on one 710 and 683; 96 tokens of 8 by popularity, 7168 x 2048 int8, where some experts
+    // have two tiles: past the caches all 162, those of one tile 165, of one or two 159)
+    if (ONCE && at.tiles > 2)
+        expert_sums<ExpertTile<C, OUT, COLS, GATHER, false>, C>(a, at, lds_address(shared), sums);
+    else
+        expert_sums<E, C>(a, at, lds_address(shared), sums);
+    E{a, at}.finish(sums);
 }
 
 // Gradient of the weights: out[e][j, c] = sum over the expert's rows of g[r, j] x[r, c].  P are
@@ -469,9 +485,9 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream, int *sums) {
 
 // Tile by the rows an expert has on average and the size of the grid, in tiles that there will be
 // at least (64 experts of 7168 channels and 2 x 2048 gated outputs, us; 3.76 GB of weights).
-//   ONCE: an expert has one row tile, and its weights are read past the caches: 16 rows 608 without
-//   and 544 with, 128 tokens of 8 experts 931 and 842 for the whole block.  With several row tiles
-//   the others read them from the caches: 192 rows 793 and 775, but the product down 453 and
+//   ONCE: experts have one row tile or two, and their weights are read past the caches: 16 rows 608
+//   without and 544 with, 128 tokens of 8 experts 931 and 842 for the whole block.  With more row
+//   tiles the others read them from the caches: 192 rows 793 and 775, but the product down 453 and
 //   469, and the gradient of x 835 and 841.  Few weights may be in the 256 MB last-level cache from
 //   the call before (22 MB: 14.3 without, 18.2 with).
 //   32 rows by 128 outputs up to 16 rows an expert (16 by 128: 544 without ONCE at 2 rows and at 4,

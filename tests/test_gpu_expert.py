@@ -699,3 +699,41 @@ def test_many_tiles_a_block_and_few_rows_between_many():
         b.check_forward(y, h, saved)
         for dtype in (torch.bfloat16, torch.float32):
             b.check_backward(saved, h, b.backward(saved, h, dtype), False)
+
+
+def _popular(T, E, popular, every):
+    """All tokens on one expert but every few, which go round the others."""
+    idx = torch.full((T, 1), popular, dtype=torch.int64, device="cuda")
+    idx[::every, 0] = torch.arange(len(range(0, T, every)), device="cuda") % E
+    return idx
+
+
+@pytest.mark.parametrize("T,E,k,n,gated", [(100, 8, 4112, 2056, False), (300, 32, 528, 4112, True),
+                                           (700, 32, 528, 4112, False)])
+def test_i8_popular_expert_beside_weights_past_the_caches(T, E, k, n, gated):
+    """More than 64 MB of weights, few rows an expert on average, one expert with many row tiles of
+    16, 32 and 64 rows and others with one or two."""
+    say("expert_i8 popular", T, E, k, n, gated)
+    gen = _gen(T)
+    idx = _popular(T, E, 5, 4)
+    h = ep.Handle(T, 1, E, 1)
+    h.layout(idx)
+    x, xs, w, ws = _i8_case(h, E, h.capacity, k, n, gen)
+    out = ref.poisoned((h.capacity, n // 2 if gated else n), torch.bfloat16)
+    h.expert_i8(x, xs, w, ws, gated=gated, out=out)
+    _check_i8(h, idx, x, xs, w, ws, gated, None, out, False, "popular")
+
+
+@pytest.mark.parametrize("token_rows", [False, True])
+def test_block_popular_expert_beside_weights_past_the_caches(token_rows):
+    T, E, H, I = 1400, 32, 520, 2056
+    b = Block(T, 1, E, 1, H, I, token_rows, False, 0.0, 31)
+    idx = _popular(T, E, 5, 20)
+    b.h.layout(idx)
+    b.idx = idx
+    b.rows, b.expert, b.token = ref.rows_of(b.h, idx)
+    gen = _gen(32)
+    b.x, b.grad = _randn(b.x.shape, gen), _randn(b.grad.shape, gen, 0.1)
+    y, h, saved = b.forward()
+    b.check_forward(y, h, saved)
+    b.check_backward(saved, h, b.backward(saved, h), False)

@@ -1,6 +1,9 @@
 """The experts' products together with layout, dispatch, combine and their gradients, as a
 serving step in 8 bits and a training step use them: against binary64, captured, and on two
 streams at once."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -234,3 +237,103 @@ def test_bound_calls_give_what_the_methods_give():
         assert torch.equal(out[rows], h.expert_i8(*h.quantize_i8(a), s.w2, s.s2)[rows])
         got = block()
         assert got[2] is None and bool(got[0][rows].isfinite().all())
+
+
+def test_one_handle_two_streams():
+    """Calls on one laid out handle only read it: two streams with their own buffers may use it at
+    once."""
+    gen = _gen(11)
+    T, K, E, H, I = 200, 2, 8, 264, 136
+    h = ep.Handle(T, K, E, 8)
+    h.layout(ref.ids(T, K, E, gen, "cuda", 0.1))
+    w13, w2 = _randn((E, 2 * I, H), gen, H ** -0.5), _randn((E, H, I), gen, I ** -0.5)
+    x = [_randn((T, H), gen) for _ in range(2)]
+    gy = [_randn((h.capacity, H), gen, 0.1) for _ in range(2)]
+    rw = torch.rand(h.capacity, generator=gen, device="cuda")
+
+    def step(i):
+        y, a, saved = h.expert_ffn(x[i], w13, w2, row_weights=rw, token_rows=True, want_saved=True)
+        gx, g13, g2, grw, _ = h.expert_ffn_backward(gy[i], x[i], w13, w2, saved, a, row_weights=rw,
+                                                    token_rows=True, want_grad_weights=True)
+        return (y, gx, grw), (g13, g2)
+
+    want = [step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(3):
+        for i, stream in enumerate(streams):
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                got[i] = step(i)
+    torch.cuda.synchronize()
+    rows = ref.rows_of(h, h.topk_idx)[0]
+    for (p, pw), (q, qw) in zip(got, want):
+        assert all(torch.equal(a[rows], b[rows]) for a, b in zip(p, q))
+        assert all(torch.equal(a, b) for a, b in zip(pw, qw))
+
+
+def test_imported_layout_gives_what_its_own_gives():
+    """A layout that came from the host, with gaps between the segments."""
+    gen = _gen(12)
+    T, K, E, H, I = 60, 3, 6, 136, 80
+    a = ep.Handle(T, K, E, 16)
+    idx = ref.ids(T, K, E, gen, "cuda", 0.1)
+    a.layout(idx)
+    own = a.read_counts()
+    b = ep.Handle(T, K, E, 16)
+    n = own["num_expanded"]
+    b.import_layout(idx, own["counts"], own["psum"], a.dst_slot.cpu().numpy(),
+                    a.src_meta[:n].cpu().numpy(), own["num_recv_tokens"])
+    w13, w2 = _randn((E, 2 * I, H), gen, H ** -0.5), _randn((E, H, I), gen, I ** -0.5)
+    x, gy = _randn((T, H), gen), _randn((a.capacity, H), gen, 0.1)
+    rows = ref.rows_of(a, idx)[0]
+    got = []
+    for h in (a, b):
+        y, act, saved = h.expert_ffn(x, w13, w2, token_rows=True, want_saved=True)
+        q, s = h.quantize_i8(act)
+        gx, g13, g2, _, _ = h.expert_ffn_backward(gy, x, w13, w2, saved, act, token_rows=True)
+        got.append((y[rows], q[rows], s[rows], gx[rows], g13, g2))
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+FIRST_CALLS = """
+import torch, combine_ep_layout_08_amd as ep
+T, K, E, H, I = 40, 2, 4, 264, 136
+g = torch.Generator(device="cuda").manual_seed(1)
+new = lambda *s: torch.randn(s, generator=g, device="cuda").mul_(0.1).bfloat16()
+idx = torch.randint(0, E, (T, K), generator=g, device="cuda")
+x, w13, w2 = new(T, H), new(E, 2 * I, H), new(E, H, I)
+i13 = torch.randint(-127, 128, (E, 2 * I, H // 16 * 16), generator=g, device="cuda", dtype=torch.int8)
+s13 = torch.rand((E, 2 * I), generator=g, device="cuda")
+h = ep.Handle(T, K, E, 8)
+h.layout(idx)
+gy = new(h.capacity, H)
+def step():
+    q, s = ep.quantize_i8(x[:, :256].contiguous())
+    act = h.expert_i8(q, s, i13[:, :, :256].contiguous(), s13, gated=True, token_rows=True)
+    y, a, saved = h.expert_ffn(x, w13, w2, token_rows=True, want_saved=True)
+    return act, y, *h.expert_ffn_backward(gy, x, w13, w2, saved, a, token_rows=True)[:3]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+for _ in range(3):
+    graph.replay()
+    torch.cuda.synchronize()
+    kept = [t.clone() for t in got]
+    rows = h.dst_slot.reshape(-1).long()
+    rows = rows[rows >= 0]
+    for p, q in zip(kept, step()):
+        if p.shape[0] == h.capacity:
+            p, q = p[rows], q[rows]
+        assert torch.equal(p, q)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Whatever a kernel needs once a device (its LDS limit) may be asked for while a graph is
+    captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True,
+                       timeout=110)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

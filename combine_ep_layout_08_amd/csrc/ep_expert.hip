@@ -113,6 +113,10 @@ enum Out { kPlain, kGated, kGateGrad };
 // The sums lie in the lanes as four outputs of one row from each matrix instruction.  Which weight
 // goes to which place of the tile is free: a lane's outputs are made consecutive, and it stores 8 of
 // them (16 bytes) at a time.
+// What bounds them (64 experts, 7168 channels, 2 x 2048 outputs and back, bf16): few rows an expert,
+// the weights' bytes, 16 rows 543 us (6.9 TB/s; up and gate) and 298 (6.3; down); many rows, the
+// card's power, 512 rows an expert 1.55 ms (1240 TFLOP/s at 1.6 GHz) and, as routing leaves
+// them, not multiples of the tile, 1.71.
 template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 struct ExpertTile {
     static constexpr bool I8 = C::Type::kBytes == 1;
@@ -288,7 +292,11 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
 }
 
 // Gradient of the weights: out[e][j, c] = sum over the expert's rows of g[r, j] x[r, c].  P are
-// the columns of x, Q those of g, the rows what is summed.
+// the columns of x, Q those of g, the rows what is summed.  An expert's rows are few chunks, so a
+// tile's sums are soon to be stored: the blocks walk the tiles in one stream of chunks, and the next
+// tile's first ones are on their way while one is stored (64 experts of 512 rows, 4096 x 7168: 2.13 ms
+// in place of 2.84 with a block a tile; 900 TFLOP/s beside 3.76 GB stored.  Without its stores the
+// kernel takes 1.7: of the 0.6 ms that their bytes take a third is hidden).
 template <typename C, bool GATHER, bool F32>
 struct GradWeightTiles {
     static constexpr int TQ = C::TQ, TP = C::TP;
@@ -400,7 +408,9 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void grad_weight_kernel(
     tile_stream<C>(tiles, lds_address(shared));
 }
 
-// The row weights' gradients from the tiles' sums, in the tiles' order.  One thread a slot.
+// The row weights' gradients from the waves' sums, in the order of their columns.  One thread a
+// slot; bound by the latency of the sums' loads, eight of which are under way at a time
+// (16 experts of 25 rows, 12 sums: the gradients of the block 43.3 us with one, 41.1).
 __global__ __launch_bounds__(256) void row_sums_kernel(const int32_t *dst, const int32_t *scalars,
                                                        int64_t num_slots, int64_t capacity,
                                                        const float *partial, int tiles,
@@ -412,8 +422,17 @@ __global__ __launch_bounds__(256) void row_sums_kernel(const int32_t *dst, const
          i += stride) {
         const int32_t row = dst[i];
         if (row < 0 || row >= capacity) continue;
+        const float *p = partial + row;
         float v = 0.0f;
-        for (int t = 0; t < tiles; ++t) v += partial[t * capacity + row];
+        int t = 0;
+        for (; t + 8 <= tiles; t += 8, p += 8 * capacity) {
+            float s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = p[j * capacity];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v += s[j];
+        }
+        for (; t < tiles; ++t, p += capacity) v += *p;
         out[row] = v;
     }
 }
@@ -536,7 +555,7 @@ int64_t grad_tiles(const GradWeightArgs &a, int size) {
 
 }  // namespace
 
-// A wave's sums are of 32 columns at least.
+// A wave's columns are 32 at least.
 int gate_grad_tiles(int32_t inter) { return (inter + 127) / 128 * 4; }
 
 hipError_t launch_expert_i8(const ExpertArgs &a, bool gated, hipStream_t stream) {

@@ -39,7 +39,7 @@ struct ExpertArgs {
     // the activation's gradient
     const void *gate_up;                     // bf16 [capacity, 2 n]
     void *grad_gate_up;                      // bf16 [capacity, 2 n]
-    float *partial;                          // [tiles of outputs, capacity] or null
+    float *partial;                          // [waves' columns, capacity] or null
 };
 
 struct GradWeightArgs {
@@ -52,7 +52,8 @@ struct GradWeightArgs {
     void *out;                               // [E, n, k]
 };
 
-// Tiles of `inter` outputs in which the activation's gradient is made.
+// At most so many waves' columns the gradient of `inter` activations is made in: a row has a
+// sum of each for the gradient of its weight.
 int gate_grad_tiles(int32_t inter);
 
 hipError_t launch_quantize_i8(const QuantI8Args &a, hipStream_t stream);

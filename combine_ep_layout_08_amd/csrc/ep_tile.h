@@ -12,6 +12,11 @@
 // row is one channel's BQ or BP values; ds_read_b64_tr_b16 hands each lane the four channels of
 // its own column.  The permutations are made by the addresses that the lanes load from, as the
 // load's place in LDS is fixed by the lane.
+//
+// In the largest tile, 256 x 256 by 8 waves of 128 x 64, a wave reads 12 KB of LDS for 32 matrix
+// instructions in a half chunk: LDS is busy a quarter to a third of the cycles, the matrix units 3 of
+// 5 to 3 of 4.  4 waves of 128 x 128 read less and are slower (512 rows an expert 1.56 ms and 1.55, the
+// gradient of x 1.66 and 1.57): one wave a SIMD has nothing to run beside its own waits.
 #pragma once
 
 #include "ep_layer_internal.h"
@@ -119,8 +124,8 @@ __device__ inline int64_t token_of(const int32_t *src_meta, int64_t row, int top
 
 // ---------------------------------------------------------------- operands
 // An operand of R rows in rows of channels.  `Threads` threads bring a chunk in kLoads loads
-// each: load i takes row i * Threads / 8 + thread / 8.  `row_of(i)` gives the row's byte offset
-// from `base` (GATHER: its address).
+// each: load i takes row i * Threads / 8 + thread / 8.  `row_of(r)` gives the bytes from `base` to
+// row r, below 2^32 but with GATHER, where the lanes hold addresses.  ONCE: past the caches.
 template <int R, int Threads, bool GATHER, bool ONCE>
 struct RowsOperand {
     static constexpr int kBytes = R * 128;

@@ -115,8 +115,8 @@ enum Out { kPlain, kGated, kGateGrad };
 // them (16 bytes) at a time.
 // What bounds them (64 experts, 7168 channels, 2 x 2048 outputs and back, bf16): few rows an expert,
 // the weights' bytes, 16 rows 543 us (6.9 TB/s; up and gate) and 298 (6.3; down); many rows, the
-// card's power, 512 rows an expert 1.55 ms (1240 TFLOP/s at 1.6 GHz) and, as routing leaves
-// them, not multiples of the tile, 1.71.
+// card's power, 512 rows an expert 1.52 ms (1265 TFLOP/s at 1.6 GHz) and, as routing leaves
+// them, not multiples of the tile, 1.70.
 template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 struct ExpertTile {
     static constexpr bool I8 = C::Type::kBytes == 1;

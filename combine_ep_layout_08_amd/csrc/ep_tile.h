@@ -63,6 +63,12 @@ __device__ inline int thread_here() {
     return t;
 }
 
+// A value that is worked out once and stays in a register.
+__device__ inline uint32_t kept(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // A value that is the same in every lane, in a scalar register.
 __device__ inline int64_t uniform(int64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
@@ -177,12 +183,21 @@ struct RowsOperand {
         const bool in = unit(thread_here()) * 16 < channels * T::kBytes;
         load_lds(stage + to + i * Threads * 16, in ? at : reinterpret_cast<const char *>(&kZeros));
     }
-    // The wave's operand of a matrix instruction: rows 16 t .., channels of 64 bytes `half`.
-    template <int TP>
-    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
-        const int lane = threadIdx.x & 63, r = 16 * t + (lane & 15);
-        return read_lds(stage + r * 128 + (((half * 4 + (lane >> 4)) ^ (r & 7)) << 4));
-    }
+    // The wave's operands of N matrix instructions, i of rows 16 (first + i STEP) ..: where in a
+    // stage the lane reads them, 64 bytes of channels `half` of them.
+    template <int N, int STEP>
+    struct Reader {
+        uint32_t at[2];
+        __device__ explicit Reader(int first) {
+            const int lane = threadIdx.x & 63, r = 16 * first + (lane & 15);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                at[h] = kept(r * 128 + (((h * 4 + (lane >> 4)) ^ (r & 7)) << 4));
+        }
+        __device__ u32x4 read(uint32_t stage, int i, int half) const {
+            return read_lds(stage + at[half] + i * STEP * 2048);
+        }
+    };
 };
 
 // An operand of C columns, channel by channel, in bf16.  CONSECUTIVE: the columns of a wave's TP
@@ -253,26 +268,41 @@ struct ColsOperand {
                             off[i]
                       : b + off[i];
     }
-    template <int TP>
-    static __device__ u32x4 fragment(uint32_t stage, int t, int half) {
-        const int lane = threadIdx.x & 63, j = lane & 15;
-        const int ch = half * 32 + (lane >> 4) * 8 + (j >> 2);
-        // four columns, of 8 bytes
-        const int piece = CONSECUTIVE ? t / TP * 4 * TP + (j & 3) * TP + t % TP : 4 * t + (j & 3);
-        u32x4 v;
+    // The wave's operands of N matrix instructions, i of columns 16 (first + i STEP) ... or their
+    // consecutive order: where in a stage the lane reads them.  What the permutation leaves apart
+    // has an address of its own, all others are constants away.
+    template <int N, int STEP>
+    struct Reader {
+        static constexpr int kWays = CONSECUTIVE ? (N + 1) / 2 : 4;
+        static_assert(CONSECUTIVE ? STEP == 1 : STEP % 2 == 0, "what the permutation does");
+        uint32_t at[kWays];
+        __device__ explicit Reader(int first) {
+            const int lane = threadIdx.x & 63, j = lane & 15;
+            const int ch = (lane >> 4) * 8 + (j >> 2);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = ch + 4 * i;
-            const uint32_t at =
-                stage + c * kRow + (((piece >> 1) ^ swizzle(c)) << 4) + (piece & 1) * 8;
-            const u32x2 r = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                           reinterpret_cast<EP_LDS s16x4 *>(static_cast<uintptr_t>(at))));
-            v[2 * i] = r.x;
-            v[2 * i + 1] = r.y;
+            for (int w = 0; w < kWays; ++w) {
+                // four columns, of 8 bytes
+                const int piece = CONSECUTIVE ? first * 4 + (j & 3) * N + 2 * w
+                                              : 4 * (first + w * STEP) + (j & 3);
+                at[w] = kept(ch * kRow + (((piece >> 1) ^ swizzle(ch)) << 4) + (piece & 1) * 8);
+            }
         }
-        return v;
-    }
+        __device__ u32x4 read(uint32_t stage, int i, int half) const {
+            const uint32_t from = stage + (CONSECUTIVE ? at[i / 2] : at[i % 4]) +
+                                  (CONSECUTIVE ? i % 2 * 8 : i / 4 * (4 * STEP * 32)) +
+                                  half * 32 * kRow;
+            u32x4 v;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {                    // swizzle(ch + 4) is swizzle(ch)
+                const u32x2 r = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<EP_LDS s16x4 *>(
+                               static_cast<uintptr_t>(from + k * 4 * kRow))));
+                v[2 * k] = r.x;
+                v[2 * k + 1] = r.y;
+            }
+            return v;
+        }
+    };
 };
 
 // ---------------------------------------------------------------- main loop
@@ -350,9 +380,11 @@ __device__ inline void tile_product(Q &q, P &p, int channels, int rows, uint32_t
     struct Half {
         u32x4 q[TQ], p[TP];
     };
+    const typename Q::template Reader<TQ, C::WQ> from_q(wq);
+    const typename P::template Reader<TP, 1> from_p(wp * TP);
     auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) {
-        if (i < TP) f.p[i] = P::template fragment<TP>(stage_p, wp * TP + i, half);
-        else f.q[i - TP] = Q::template fragment<TP>(stage_q, (i - TP) * C::WQ + wq, half);
+        if (i < TP) f.p[i] = from_p.read(stage_p, i, half);
+        else f.q[i - TP] = from_q.read(stage_q, i - TP, half);
     };
     // Multiplies `now`, a row tile at a time, while `then` is read and, with LOAD, the N loads of
     // a chunk set out.  Issued all at once the loads take the address unit 16 cycles each, in
@@ -537,9 +569,11 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
     struct Half {
         u32x4 q[TQ], p[TP];
     };
+    const typename Q::template Reader<TQ, C::WQ> from_q(wq);
+    const typename P::template Reader<TP, 1> from_p(wp * TP);
     auto read = [&](Half &f, uint32_t stage_q, uint32_t stage_p, int half, int i) EP_INLINE {
-        if (i < TP) f.p[i] = P::template fragment<TP>(stage_p, wp * TP + i, half);
-        else f.q[i - TP] = Q::template fragment<TP>(stage_q, (i - TP) * C::WQ + wq, half);
+        if (i < TP) f.p[i] = from_p.read(stage_p, i, half);
+        else f.q[i - TP] = from_q.read(stage_q, i - TP, half);
     };
     typename C::Sums sums;
     // Multiplies `f`, a row tile at a time, while `b` is read and the N loads of a chunk set out.

@@ -111,8 +111,8 @@ enum Out { kPlain, kGated, kGateGrad };
 //   kGateGrad  the sums are the gradient of the activation; gate and up are read, their
 //              gradients stored
 // The sums lie in the lanes as four outputs of one row from each matrix instruction.  Which weight
-// goes to which place of the tile is free: a lane's outputs are made consecutive, and it stores 8 of
-// them (16 bytes) at a time.
+// goes to which place of the tile is free: a lane's outputs of two instructions are made consecutive,
+// and it stores these 8 (16 bytes) at a time, the four lanes of a row 64 bytes that lie together.
 // What bounds them (64 experts, 7168 channels, 2 x 2048 outputs and back, bf16): few rows an expert,
 // the weights' bytes, 16 rows 543 us (6.9 TB/s; up and gate) and 298 (6.3; down); many rows, the
 // card's power, 512 rows an expert 1.52 ms (1265 TFLOP/s at 1.6 GHz) and, as routing leaves
@@ -154,7 +154,8 @@ struct ExpertTile {
             // instructions of the upper half are up's
             p.init(w, [&](int r) {
                 const int i = r % 16, t = r / 16 % TP;
-                int j = p0 + r / (16 * TP) * 16 * G + i / 4 * 4 * G + t % G * 4 + i % 4;
+                const int g = t % G * 4;                     // of the lane part's outputs
+                int j = p0 + r / (16 * TP) * 16 * G + g / U * 4 * U + i / 4 * U + g % U + i % 4;
                 j = j < a.n ? j : a.n - 1;                   // computed on, and not stored
                 return (j + (t < G ? 0 : a.n)) * pitch;
             });
@@ -182,7 +183,7 @@ struct ExpertTile {
     __device__ void finish(const typename C::Sums &sums) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int wq = wave / C::WP, wp = wave % C::WP, lane = threadIdx.x & 63;
-        const int col0 = at.column * BP + wp * 16 * G + (lane >> 4) * 4 * G;     // the lane's first output
+        const int col0 = at.column * BP + wp * 16 * G + (lane >> 4) * U;     // the lane's first output
         const int64_t w_at = at.expert * ((OUT == kGated ? 2 : 1) * static_cast<int64_t>(a.n));
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
@@ -198,7 +199,7 @@ struct ExpertTile {
             if (OUT != kPlain && a.row_weights && in) w = a.row_weights[row];
 #pragma unroll
             for (int u = 0; u < 4 * G; u += U) {             // of the lane's outputs
-                const int col = col0 + u;
+                const int col = col0 + 4 * u;
                 if (!in || col >= a.n) continue;
                 float v[U], up[U];
 #pragma unroll
@@ -382,7 +383,7 @@ struct GradWeightTiles {
     }
     EP_INLINE __device__ bool finish(const At &at, const typename C::Sums &sums) {
         const int lane = thread_here() & 63;
-        const int c0 = at.p0 + wp * 16 * TP + (lane >> 4) * 4 * TP;      // the lane's first column
+        const int c0 = at.p0 + wp * 16 * TP + (lane >> 4) * 8;      // the lane's first column
 #pragma unroll
         for (int t = 0; t < TQ; ++t) {
             const int j = at.q0 + (t * C::WQ + wq) * 16 + (lane & 15);
@@ -390,14 +391,14 @@ struct GradWeightTiles {
             const int64_t to = (static_cast<int64_t>(at.expert) * a.n + j) * a.k + c0;
 #pragma unroll
             for (int u = 0; u < TP; u += 2) {
-                if (c0 + 4 * u >= a.k) continue;
+                if (c0 + 16 * u >= a.k) continue;
                 const f32x4 v = sums.v[t][u], w = sums.v[t][u + 1];
                 if (F32) {
-                    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to + 4 * u);
+                    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to + 16 * u);
                     o[0] = v;
                     o[1] = w;
                 } else {
-                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + to + 4 * u) =
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + to + 16 * u) =
                         u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(w[0], w[1]),
                               pack2(w[2], w[3])};
                 }

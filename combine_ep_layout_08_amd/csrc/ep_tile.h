@@ -200,9 +200,9 @@ struct RowsOperand {
     };
 };
 
-// An operand of C columns, channel by channel, in bf16.  CONSECUTIVE: the columns of a wave's TP
+// An operand of C columns, channel by channel, in bf16.  CONSECUTIVE: the columns of two of a wave's
 // matrix instructions are dealt out so that a lane's sums lie side by side, part l / 16 of the
-// wave's columns having 4 in each instruction: the transposing read takes any four columns
+// lanes having 8 of their 32, 4 in each instruction: the transposing read takes any four columns
 // that lie together.
 template <int C, int Threads, bool GATHER, bool CONSECUTIVE, bool ONCE>
 struct ColsOperand {
@@ -221,9 +221,9 @@ struct ColsOperand {
     static __device__ int channel(int i, int thread) { return (i * Threads + thread) / (kRow / 16); }
     // Units of 16 bytes are permuted by these bits of the channel.  A read takes four times
     // 8 bytes of four consecutive channels in each row of 16 lanes: 32 bytes of a channel, or
-    // CONSECUTIVE four pieces 32 bytes apart.
+    // CONSECUTIVE four pieces 16 bytes apart.
     static __device__ int swizzle(int ch) {
-        return CONSECUTIVE ? (ch & 1) | ((ch << 2) & 8) : ((ch & 3) | ((ch >> 1) & 4)) << 1;
+        return CONSECUTIVE ? (ch & 3) << 2 : ((ch & 3) | ((ch >> 1) & 4)) << 1;
     }
 
     // Columns `first` .. of `cols` (in a row of `pitch` bytes) from channel 0 at `b`.
@@ -273,8 +273,9 @@ struct ColsOperand {
     // has an address of its own, all others are constants away.
     template <int N, int STEP>
     struct Reader {
-        static constexpr int kWays = CONSECUTIVE ? (N + 1) / 2 : 4;
-        static_assert(CONSECUTIVE ? STEP == 1 : STEP % 2 == 0, "what the permutation does");
+        static constexpr int kWays = CONSECUTIVE ? N / 2 : 4;
+        static_assert(CONSECUTIVE ? STEP == 1 && N % 2 == 0 : STEP % 2 == 0,
+                      "what the permutation does");
         uint32_t at[kWays];
         __device__ explicit Reader(int first) {
             const int lane = threadIdx.x & 63, j = lane & 15;
@@ -282,7 +283,7 @@ struct ColsOperand {
 #pragma unroll
             for (int w = 0; w < kWays; ++w) {
                 // four columns, of 8 bytes
-                const int piece = CONSECUTIVE ? first * 4 + (j & 3) * N + 2 * w
+                const int piece = CONSECUTIVE ? first * 4 + (j & 3) * 2 + 8 * w
                                               : 4 * (first + w * STEP) + (j & 3);
                 at[w] = kept(ch * kRow + (((piece >> 1) ^ swizzle(ch)) << 4) + (piece & 1) * 8);
             }

@@ -542,7 +542,6 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
     };
     // Chunks until so many have set out.
     auto fill_q = [&](int count) EP_INLINE {
-        bool some = false;
 #pragma clang loop unroll(disable)
         while (lq.count < count) {
             const int left = next_q();
@@ -550,12 +549,9 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
 #pragma unroll
             for (int i = 0; i < NQ; ++i) load_q(left, i);
             loaded_q(left);
-            some = true;
         }
-        return some;
     };
     auto fill_p = [&](int count) EP_INLINE {
-        bool some = false;
 #pragma clang loop unroll(disable)
         while (lp.count < count) {
             const int left = next_p();
@@ -563,9 +559,7 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) load_p(left, i);
             loaded_p(left);
-            some = true;
         }
-        return some;
     };
     struct Half {
         u32x4 q[TQ], p[TP];
@@ -620,12 +614,14 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
             const int left_p = lp.count < g + C::SP ? next_p() : 0;
             step(first, second, at_q, at_p, 1, Int<NP>(), [&](int i) EP_INLINE { load_p(left_p, i); });
             loaded_p(left_p);
-            // chunk g + 1 has come: BQ chunks of Q and BP of P may still be on their way, and
-            // what was stored since
-            const bool known = lq.count == g + C::SQ && lp.count == g + C::SP && stores >= 0;
-            if (!known) wait_loads<0>();
-            else if (stores > 0) wait_loads<BQ * NQ + BP * NP + S::kStores>();
-            else wait_loads<BQ * NQ + BP * NP>();
+            // chunk g + 1 has come: BQ chunks of Q and BP of P (none where the tiles ahead have no
+            // more) may still be on their way, and what was stored since
+            const bool known = lq.count == g + C::SQ && stores >= 0;
+            const bool all = known && lp.count == g + C::SP, next = known && lp.count == g + 2;
+            if (all && stores > 0) wait_loads<BQ * NQ + BP * NP + S::kStores>();
+            else if (all) wait_loads<BQ * NQ + BP * NP>();
+            else if (next && stores > 0) wait_loads<BQ * NQ + S::kStores>();
+            else wait_loads<0>();
             stores = 0;
             block_barrier();
             at_q = at_q + C::kStageQ == ring_p ? ring_q : at_q + C::kStageQ;
@@ -635,14 +631,20 @@ __device__ inline void tile_stream(S &src, uint32_t lds) {
             step(second, first, at_q, at_p, 0, Int<NQ>(), [&](int i) EP_INLINE { load_q(left_q, i); });
             loaded_q(left_q);
         }
-        stores = src.finish(now, sums) ? S::kStores : -1;
-        if (!more) return;
-        now = then;                              // both operands have begun with it
-        lq.ahead = lp.ahead = false;
-        more = fetch(then);
-        // tiles of few chunks: what the loaders could not see before
-        if (fill_q(g + C::SQ)) stores = -1;
-        if (fill_p(g + C::SP - 1)) stores = -1;
+        // Tiles of few chunks: what the loaders could not see before sets out ahead of the stores,
+        // which loads behind them would wait for (all gradients of the block, 64 experts of 16 rows,
+        // 7168 and 2048 channels: 2212 -> 2146 us; of 512 rows 6266 -> 6236).
+        const At done = now;
+        const bool end = !more;
+        if (!end) {
+            now = then;                          // both operands have begun with it
+            lq.ahead = lp.ahead = false;
+            more = fetch(then);
+            fill_q(g + C::SQ);
+            fill_p(g + C::SP - 1);
+        }
+        stores = src.finish(done, sums) ? S::kStores : -1;
+        if (end) return;
     }
 }
 

@@ -737,3 +737,32 @@ def test_block_popular_expert_beside_weights_past_the_caches(token_rows):
     y, h, saved = b.forward()
     b.check_forward(y, h, saved)
     b.check_backward(saved, h, b.backward(saved, h), False)
+
+
+@pytest.mark.parametrize("rows", ["one chunk", "one or two", "one to three, some none"])
+@pytest.mark.parametrize("token_rows", [False, True])
+def test_weight_gradients_of_full_tiles_and_few_rows(rows, token_rows):
+    """Weight gradients in full tiles, several a block, of so few rows that a tile is stored while the
+    next ones' first rows are on their way."""
+    say("weight gradients", rows, token_rows)
+    E, H, I = 96, 1024, 512
+    most = {"one chunk": 64, "one or two": 128}.get(rows, 192)
+    gen = torch.Generator().manual_seed(most)
+    counts = torch.randint(0 if most == 192 else 1, most + 1, (E,), generator=gen)
+    if most == 192:
+        counts[torch.rand(E, generator=gen) < 0.3] = 0
+    ids = torch.repeat_interleave(torch.arange(E), counts)
+    idx = ids[torch.randperm(len(ids), generator=gen)][:, None].cuda()
+    b = Block(len(ids), 1, E, 1, H, I, token_rows, False, 0.0, most)
+    b.h.layout(idx)
+    b.idx = idx
+    b.rows, b.expert, b.token = ref.rows_of(b.h, idx)
+    dev = _gen(most)
+    b.x, b.grad = _randn(b.x.shape, dev), _randn(b.grad.shape, dev, 0.1)
+    y, h, saved = b.forward()
+    for dtype in (torch.bfloat16, torch.float32):
+        first = b.backward(saved, h, dtype)
+        b.check_backward(saved, h, first, False)
+        for _ in range(3):
+            again = b.backward(saved, h, dtype)
+            assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])

@@ -102,7 +102,8 @@ __global__ __launch_bounds__(256) void quant_i8_kernel(const QuantI8Args a, int6
 
 template <int W, int V, bool MANY = false>
 hipError_t launch_quant(const QuantI8Args &a, hipStream_t stream) {
-    constexpr int64_t kMost = int64_t(1) << 24;      // rows; fewer than 2^32 threads a launch
+    // rows of a launch: 2^22 blocks, so 2^30 threads whatever a row takes (HIP refuses 2^32)
+    constexpr int64_t kMost = (int64_t(1) << 22) * (4 / W);
     for (int64_t r = 0; r < a.num_rows; r += kMost) {
         const int64_t n = a.num_rows - r < kMost ? a.num_rows - r : kMost;
         const int64_t blocks = (n * W + 3) / 4;

@@ -504,7 +504,8 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream, int *sums) {
     const int across = (a.n + BP - 1) / BP;
     const int64_t tiles = row_tiles(a.seg, C::BQ) * across;
     if (sums) *sums = across * C::WP;
-    if constexpr (!COLS) {
+    // the block's product back down reads h, which has no tokens' own rows
+    if constexpr (!COLS && (OUT == kGated || C::Type::kBytes == 1)) {
         if (a.token_rows)
             return launch_tiles<C, expert_kernel<C, OUT, COLS, true, ONCE>>(a, tiles, stream);
     }
@@ -544,8 +545,10 @@ hipError_t choose_expert(const ExpertArgs &a, hipStream_t stream, int *sums = nu
     }
     if (slots > 16 * experts && tiles(64, 128) >= 512) {
         typedef Tile<T, 64, 128, 2, 2, 3, 3> C;
-        return once ? launch_expert<C, OUT, COLS, true>(a, stream, sums)
-                    : launch_expert<C, OUT, COLS, false>(a, stream, sums);
+        // in columns never once: up to 48 rows an expert 512 of these tiles are 256 large ones
+        if constexpr (!COLS)
+            if (once) return launch_expert<C, OUT, COLS, true>(a, stream, sums);
+        return launch_expert<C, OUT, COLS, false>(a, stream, sums);
     }
     if (tiles(32, 128) >= 512) {
         typedef Tile<T, 32, 128, 1, 4, 4, 4> C;

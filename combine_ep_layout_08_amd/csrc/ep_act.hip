@@ -16,13 +16,6 @@ dim3 act_grid(int64_t waves) {
     return dim3(static_cast<uint32_t>(blocks < kActBlocks ? blocks : kActBlocks));
 }
 
-// 1 / (1 + exp(-g)): v_exp_f32 and v_rcp_f32 are within an ulp of binary32, and the
-// argument's rounding adds |g| 2^-24: far inside the outputs' 8 or 16 bits.
-// exp(-g) = inf (g < -88) gives 0.
-__device__ inline float sigmoid(float g) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
-}
-
 // Exponent bytes of gate's and up's block b into a row of 2 * blocks bytes: up's
 // need not start at a pack, so every block stores its own byte; the bytes behind the
 // last block are zero.

@@ -9,11 +9,6 @@
 namespace ep {
 namespace {
 
-// 1 / (1 + exp(-g)), as ep_swiglu has it.
-__device__ inline float sigmoid(float g) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
-}
-
 // ---------------------------------------------------------------- tiles of the experts' rows
 // Every expert's rows are cut into as few row tiles of at most `per` rows as they need, about
 // equal ones, and every row tile meets `across` tiles of outputs.

@@ -29,7 +29,8 @@ __device__ inline uint32_t wave_max(uint32_t v) {
 
 // Eight codes of one row: v / s, rounded to the nearest whole number.  q0 + (v - q0 s) y, each
 // step one fused operation and y the correctly rounded reciprocal, is the correctly rounded
-// quotient (Markstein, IBM Journal of Research and Development 34, 1990); adding and taking off 1.5 2^23 rounds it.
+// quotient (Markstein, IBM Journal of Research and Development 34, 1990); adding 1.5 2^23 rounds it, and
+// the sum's low byte is the code.
 __device__ inline u32x2 codes8(const u32x4 v, float s, float y) {
 #pragma clang fp contract(off)
     float f[8];

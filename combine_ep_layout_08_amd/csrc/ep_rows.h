@@ -1,5 +1,5 @@
 // Device helpers of the layer operators: bf16 and E4M3 rows in 16-byte
-// vectors, block scales, and sums over a wave.
+// vectors, block scales, sums over a wave, and the activation's sigmoid.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -96,6 +96,13 @@ __device__ inline double wave_sum64(double v) {
     v += row_ror64<1>(v);
     return (lane_value64(v, 0) + lane_value64(v, 16)) +
            (lane_value64(v, 32) + lane_value64(v, 48));
+}
+
+// 1 / (1 + exp(-g)): v_exp_f32 and v_rcp_f32 are within an ulp of binary32, and the
+// argument's rounding adds |g| 2^-24: far inside the outputs' 8 or 16 bits.
+// exp(-g) = inf (g < -88) gives 0.
+__device__ inline float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
 // ---------------------------------------------------------------- E4M3 blocks

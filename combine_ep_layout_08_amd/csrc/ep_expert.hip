@@ -110,8 +110,12 @@ enum Out { kPlain, kGated, kGateGrad };
 // and it stores these 8 (16 bytes) at a time, the four lanes of a row 64 bytes that lie together.
 // What bounds them (64 experts, 7168 channels, 2 x 2048 outputs and back, bf16): few rows an expert,
 // the weights' bytes, 16 rows 543 us (6.9 TB/s; up and gate) and 298 (6.3; down); many rows, the
-// card's power, 512 rows an expert 1.52 ms (1265 TFLOP/s at 1.6 GHz) and, as routing leaves
-// them, not multiples of the tile, 1.70.
+// matrix units and the clock that the card holds under them: 512 rows an expert 1.48 to 1.52 ms (1265
+// to 1300 TFLOP/s; matrix units busy 73 % of the cycles at 1.7 to 1.8 of 2.4 GHz) and, as routing
+// leaves them, not multiples of the tile, 1.61 to 1.70 (64 %).  GATHER's addresses are two registers
+// a load: its tiles of 256 x 256 spill 6 or 7, around the last chunks (int8 prompt of 4096 tokens,
+// 8 of 64 experts: 900 us from the tokens' own rows, 888 from expanded ones; the bf16 block 2583 and
+// 2601).
 template <typename C, int OUT, bool COLS, bool GATHER, bool ONCE>
 struct ExpertTile {
     static constexpr bool I8 = C::Type::kBytes == 1;
@@ -292,7 +296,16 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void expert_kernel(const E
 // tile's sums are soon to be stored: the blocks walk the tiles in one stream of chunks, and the next
 // tile's first ones are on their way while one is stored (64 experts of 512 rows, 4096 x 7168: 2.10 ms
 // in place of 2.84 with a block a tile; 900 TFLOP/s beside 3.76 GB stored.  Without its stores the
-// kernel takes 1.7: of the 0.6 ms that their bytes take a third is hidden).
+// kernel takes 1.7: of the 0.6 ms that their bytes take a third is hidden).  The matrix units are busy
+// 40 % of the cycles, at 2.1 GHz: products and stores of a compute unit's one block follow each other.
+// Known to be left (4096 tokens, uneven rows, w13 of 7168 to 2 x 2048 channels):
+//   an XCD's eighth of the tiles is of whole experts, so popular ones keep their XCD busy after the
+//   others (popularity by rank^-1.2 beside uniform: 64 experts, 8 a token, 3.78 ms and 2.46; 16, 2 a
+//   token, 1.20 and 0.58; 8, 1 a token, 0.65 and 0.31);
+//   GATHER: a load's address is a token's number that is read just before, which waits for all loads
+//   under way, four times a chunk (3.54 ms beside 2.46 from expanded rows);
+//   fp32 gradients are twice the bytes (all gradients of the block 7.29 ms and 6.17; 128 tokens 3.01 and
+//   2.15).
 template <typename C, bool GATHER, bool F32>
 struct GradWeightTiles {
     static constexpr int TQ = C::TQ, TP = C::TP;
@@ -520,6 +533,9 @@ hipError_t launch_expert(const ExpertArgs &a, hipStream_t stream, int *sums) {
 //   by 128, 780 with 128 by 256, 677).  Weights in columns are read in pieces of 512 bytes by tiles of
 //   256 outputs, of 256 by tiles of 128: the gradient of the activation 16 rows 343 with 32 by 128,
 //   316 with 256 by 256.
+//   Large tiles from 256 of them on, one a compute unit.  Below that long sums would gain by them and
+//   short ones lose (int8, 8 experts of 512 rows, 7168 to 2048 channels, 128 large tiles: 95 with 64 by
+//   128, 81 with 256 by 256; 1024 to 2048 17 and 21; 64 large tiles, 7168 to 1024 37 and 68).
 //   A grid that does not fill the card takes smaller tiles (16 experts, 25 rows, 648 channels, 2 x 360
 //   outputs and back: 15.6 with 32 by 128, 14.3 with 16 by 128; one token of 8 experts 124 and 122).
 template <typename T, int OUT, bool COLS>

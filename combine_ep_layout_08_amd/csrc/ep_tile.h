@@ -14,8 +14,8 @@
 // load's place in LDS is fixed by the lane.
 //
 // In the largest tile, 256 x 256 by 8 waves of 128 x 64, a wave reads 12 KB of LDS for 32 matrix
-// instructions in a half chunk: LDS is busy a quarter to a third of the cycles, the matrix units 3 of
-// 5 to 3 of 4.  4 waves of 128 x 128 read less and are slower (512 rows an expert 1.56 ms and 1.55, the
+// instructions in a half chunk: LDS is busy a quarter to a third of the cycles, the matrix units
+// half of them (512 rows an expert, uneven, weights in columns) to 3 of 4 (even, in rows).  4 waves of 128 x 128 read less and are slower (512 rows an expert 1.56 ms and 1.55, the
 // gradient of x 1.66 and 1.57): one wave a SIMD has nothing to run beside its own waits.
 #pragma once
 
@@ -34,8 +34,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // 16 x 16 outputs of 64 bytes of channels: lane l holds p = l % 16 of the first operand, q =
 // l % 16 of the second, the 16 bytes of channels at 16 (l / 16) of both, and the outputs
 // p = 4 (l / 16) + i of q = l % 16.  (Instructions of 32 x 32 outputs: 1.62 ms in place of 1.55 for
-// 64 experts of 512 rows, 7168 to 4096 channels, at 1.56 GHz in place of 1.62: the
-// card's power is what bounds a product of these sizes; on zeros both run a sixth faster.)
+// 64 experts of 512 rows, 7168 to 4096 channels, at a clock 4 % lower; on zeros both run a sixth
+// faster: the clock that the card holds, 1.7 to 1.8 of its 2.4 GHz here, is part of what bounds
+// a product of these sizes.)
 struct Bf16 {
     typedef f32x4 Acc;
     static constexpr int kBytes = 2;

@@ -68,7 +68,7 @@ ep_status ep_quantize_i8_rows(const ep_handle *h, const void *x, int32_t channel
  *            1: x is [num_tokens, k] and an expanded row reads its slot's token.
  *   w        device int8 [E, n, k], 16-byte aligned; n % 8 == 0 (gated: n % 16 == 0),
  *            n <= 65536.
- *   w_scale  device fp32 [E, n].
+ *   w_scale  device fp32 [E, n], 16-byte aligned.
  *   row_weights  NULL (weight 1) or, gated, fp32 [capacity].
  *   out      device bf16 [capacity, n] (gated: [capacity, n/2]), 16-byte aligned.
  */
